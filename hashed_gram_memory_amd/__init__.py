@@ -560,3 +560,6 @@ def probe_rows(plan: Plan, addr: torch.Tensor, out: torch.Tensor, stream=None) -
     _check(measure_lib().engram_probe_rows(plan.handle, _dev(addr, torch.uint32, "addr"), addr.shape[0],
                                   _dev(out, torch.float32, "out"), _stream(stream)), "engram_probe_rows")
     return out
+
+
+from .serving import kv_append, paged_attention, qk_norm_rope  # noqa: E402  (the binding above comes first)

@@ -1,0 +1,312 @@
+// Head norm, rotation by position, and the append into a paged cache.
+//
+// A head row x of dim D (one token, one head):
+//     y_j = x_j * rsqrt(sum_j x_j^2 / D + eps) * w_j           (w given)
+//     (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t)
+// for the R/2 pairs (a, b) of the first R elements, t = position *
+// inv_freq[pair]; pairs are (i, i + R/2), or (2i, 2i + 1) when interleaved.
+// Everything is fp32 and rounded once at the store; the angle is reduced to
+// a fraction of a turn in fp64, so that a position of a million keeps all of
+// fp32's digits in cos and sin (in fp32 the product alone would be off by
+// 0.03 rad there).
+//
+// The kernels read each row once and write it once: HBM-bound for prompts,
+// launch-bound for single tokens.
+//
+// Mapping: D/16 lanes hold a row (16 elements each), so a wave holds 16 to 4
+// rows of one token.  A rotating lane takes the 8-element blocks j and
+// j + R/16: in the half form both elements of a pair are then in one lane and
+// no lane exchanges anything but the norm's sum (2 to 4 cross-lane adds); in
+// the interleaved form each block holds its own pairs.  Either way a lane
+// needs 8 cosines and sines, computed once and used for every row that the
+// wave takes of its token.
+#include "serving.h"
+
+namespace engram {
+namespace {
+
+constexpr double kInvTwoPi = 0.15915494309189533576888;
+
+struct Turn {
+    float c[8], s[8];  // of block 0's pairs, then (interleaved) block 1's
+};
+
+__device__ __forceinline__ Turn load_turn(const double* __restrict__ inv_freq, int32_t pos, uint32_t j, uint32_t rb,
+                                          bool interleaved) {
+    Turn t;
+    const double p = static_cast<double>(pos) * kInvTwoPi;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t i = interleaved ? (e < 4 ? 4u * j + e : 4u * (j + rb) + (e - 4)) : 8u * j + e;
+        const double turns = p * inv_freq[i];
+        const float f = static_cast<float>(turns - __builtin_rint(turns));  // [-1/2, 1/2]
+        sincospif(2.0f * f, &t.s[e], &t.c[e]);
+    }
+    return t;
+}
+
+template <class T>
+__device__ __forceinline__ void unpack8(u32x4v w, float* x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = T::lo(w[i]);
+        x[2 * i + 1] = T::hi(w[i]);
+    }
+}
+
+template <class T>
+__device__ __forceinline__ u32x4v pack8(const float* x) {
+    u32x4v w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = T::pack(x[2 * i], x[2 * i + 1]);
+    return w;
+}
+
+// Norm over the row's LPH lanes; x: blocks 0 and 1 of this lane.
+template <int LPH>
+__device__ __forceinline__ void norm_row(float* x, const float* w, float eps) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor(ss, m);
+    const float r = 1.0f / __builtin_sqrtf(ss * (1.0f / (16 * LPH)) + eps);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
+}
+
+__device__ __forceinline__ void turn_row(float* x, const Turn& t, bool interleaved) {
+    if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = x[2 * e], b = x[2 * e + 1];
+            x[2 * e] = a * t.c[e] - b * t.s[e];
+            x[2 * e + 1] = a * t.s[e] + b * t.c[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = x[e], b = x[8 + e];
+            x[e] = a * t.c[e] - b * t.s[e];
+            x[8 + e] = a * t.s[e] + b * t.c[e];
+        }
+    }
+}
+
+// The two 8-element blocks of lane j of a row (rb = R/16 lanes rotate).
+struct Blocks {
+    uint32_t b0, b1;
+};
+__device__ __forceinline__ Blocks blocks_of(uint32_t j, uint32_t rb) {
+    return j < rb ? Blocks{j, j + rb} : Blocks{2u * j, 2u * j + 1u};
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs A, uint32_t tok_base,
+                                                        uint32_t tok_end, uint32_t chunks, uint32_t iters) {
+    constexpr int LPH = D / 16, RPW = 64 / LPH;
+    const uint32_t item = blockIdx.x * 4u + (threadIdx.x >> 6);
+    const uint32_t of_launch = item / chunks, chunk = item - of_launch * chunks;
+    const uint32_t tok = tok_base + of_launch;
+    if (tok >= tok_end) return;
+    const uint32_t lane = threadIdx.x & 63u, j = lane & (LPH - 1u);
+    const uint32_t rb = A.rotary / 16u;
+    const bool il = A.interleaved != 0, turns = j < rb;
+    const Blocks b = blocks_of(j, rb);
+    Turn t;
+    if (turns) t = load_turn(A.inv_freq, A.positions[tok], j, rb, il);
+    const uint32_t total = A.heads[0] + A.heads[1];
+    for (uint32_t it = 0; it < iters; ++it) {
+        const uint32_t row = (chunk * iters + it) * RPW + lane / LPH;
+        const bool live = row < total;
+        const uint32_t which = row < A.heads[0] ? 0u : 1u;
+        const uint32_t head = which ? row - A.heads[0] : row;
+        float x[16];
+        if (live) {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(which ? A.src[1] : A.src[0]) +
+                                  tok * (which ? A.src_tok[1] : A.src_tok[0]) +
+                                  head * (which ? A.src_head[1] : A.src_head[0]);
+            unpack8<T>(*reinterpret_cast<const u32x4v*>(src + b.b0 * 8u), x);
+            unpack8<T>(*reinterpret_cast<const u32x4v*>(src + b.b1 * 8u), x + 8);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+        }
+        const uint16_t* wp = reinterpret_cast<const uint16_t*>(which ? A.weight[1] : A.weight[0]);
+        if (wp) {  // the same for all lanes of a row
+            float w[16];
+            unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + b.b0 * 8u), w);
+            unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + b.b1 * 8u), w + 8);
+            norm_row<LPH>(x, w, A.eps);
+        }
+        if (turns) turn_row(x, t, il);
+        if (live) {
+            uint16_t* dst = reinterpret_cast<uint16_t*>(which ? A.dst[1] : A.dst[0]) +
+                            tok * (which ? A.dst_tok[1] : A.dst_tok[0]) + head * (which ? A.dst_head[1] : A.dst_head[0]);
+            *reinterpret_cast<u32x4v*>(dst + b.b0 * 8u) = pack8<T>(x);
+            *reinterpret_cast<u32x4v*>(dst + b.b1 * 8u) = pack8<T>(x + 8);
+        }
+    }
+}
+
+// Eight e4m3 codes of x * 448 / amax, nearest even.  x * 448 is exact for
+// 16-bit inputs (448 = 7 * 2^6) and the division is correctly rounded, so a
+// quotient half-way between two codes is seen as such.
+__device__ __forceinline__ u32x2v encode8(const float* x, float amax) {
+    // keep x * 448 finite: a power of two taken from both changes nothing
+    const float down = amax >= 0x1p100f ? 0x1p-64f : 1.0f;
+    const float d = amax > 0.0f ? amax * down : (amax == 0.0f ? 1.0f : amax);
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = (x[e] * down) * 448.0f / d;
+    u32x2v w;
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    w[0] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true));
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+    w[1] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true));
+    return w;
+}
+
+template <class T, int D, bool kE4m3>
+__global__ __launch_bounds__(256) void append_kernel(const AppendArgs A, uint32_t tok_base,
+                                                     uint32_t tok_end, uint32_t chunks, uint32_t iters) {
+    constexpr int LPH = D / 16, RPW = 64 / LPH;
+    const uint32_t item = blockIdx.x * 4u + (threadIdx.x >> 6);
+    const uint32_t of_launch = item / chunks, chunk = item - of_launch * chunks;
+    const uint32_t tok = tok_base + of_launch;
+    if (tok >= tok_end) return;
+    const int64_t slot = A.slots[tok];
+    // padding (negative) and slots past the pool are skipped
+    if (slot < 0 || (slot >> A.cache.page_shift) >= A.cache.n_pages) return;
+    const int64_t page = slot >> A.cache.page_shift;
+    const uint32_t at = static_cast<uint32_t>(slot) & ((1u << A.cache.page_shift) - 1u);
+    const uint32_t lane = threadIdx.x & 63u, j = lane & (LPH - 1u);
+    const uint32_t rb = A.rotary / 16u;
+    const bool il = A.interleaved != 0, turns = j < rb;
+    const Blocks b = blocks_of(j, rb);
+    Turn t;
+    if (turns) t = load_turn(A.inv_freq, A.positions[tok], j, rb, il);
+    const uint32_t heads = A.cache.n_kv_heads, total = 2u * heads;
+    float w[16];
+    if (A.weight) {
+        const uint16_t* wp = reinterpret_cast<const uint16_t*>(A.weight);
+        unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + b.b0 * 8u), w);
+        unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + b.b1 * 8u), w + 8);
+    }
+    for (uint32_t it = 0; it < iters; ++it) {
+        const uint32_t row = (chunk * iters + it) * RPW + lane / LPH;
+        const bool live = row < total;
+        const uint32_t which = row < heads ? 0u : 1u;
+        const uint32_t head = which ? row - heads : row;
+        u32x4v r0 = {0u, 0u, 0u, 0u}, r1 = r0;
+        if (live) {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(which ? A.src[1] : A.src[0]) +
+                                  tok * (which ? A.src_tok[1] : A.src_tok[0]) +
+                                  head * (which ? A.src_head[1] : A.src_head[0]);
+            r0 = *reinterpret_cast<const u32x4v*>(src + b.b0 * 8u);
+            r1 = *reinterpret_cast<const u32x4v*>(src + b.b1 * 8u);
+        }
+        float x[16];
+        unpack8<T>(r0, x);
+        unpack8<T>(r1, x + 8);
+        if (which == 0) {  // the same for all lanes of a row; a value row keeps its bits
+            if (A.weight) norm_row<LPH>(x, w, A.eps);
+            if (turns) turn_row(x, t, il);
+            if (!kE4m3) {
+                r0 = pack8<T>(x);
+                r1 = pack8<T>(x + 8);
+            }
+        }
+        const int64_t line = (static_cast<int64_t>(head) << A.cache.page_shift) + at;  // of the page's rows
+        if (kE4m3) {
+            // the largest magnitude by its bits, so that a NaN is the largest of all and reaches the scale
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = max(m, __builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int k = 1; k < LPH; k <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), k)));
+            const float amax = __builtin_bit_cast(float, m);
+            if (live) {
+                uint8_t* dst = (which ? A.cache.v + page * A.cache.v_page_stride : A.cache.k + page * A.cache.k_page_stride) +
+                               line * D;
+                *reinterpret_cast<u32x2v*>(dst + b.b0 * 8u) = encode8(x, amax);
+                *reinterpret_cast<u32x2v*>(dst + b.b1 * 8u) = encode8(x + 8, amax);
+                if (j == 0) {
+                    float* sc = which ? A.cache.v_scale : A.cache.k_scale;
+                    sc[((page * heads) << A.cache.page_shift) + line] = amax / 448.0f;
+                }
+            }
+        } else if (live) {
+            uint16_t* dst = reinterpret_cast<uint16_t*>(which ? A.cache.v : A.cache.k) +
+                            page * (which ? A.cache.v_page_stride : A.cache.k_page_stride) + line * D;
+            *reinterpret_cast<u32x4v*>(dst + b.b0 * 8u) = r0;
+            *reinterpret_cast<u32x4v*>(dst + b.b1 * 8u) = r1;
+        }
+    }
+}
+
+// Tokens per launch from which a wave takes all rows of its token (the
+// cosines are then computed once per token); below it each wave takes one step
+// of rows, so that a few tokens still spread over the chip.
+constexpr uint32_t kManyTokens = 2048;
+
+// kernel(args, tok_base, tok_end, chunks, iters) over all tokens; a launch
+// has at most 2^24 waves, so that its grid stays below 2^32 threads.
+template <class Args>
+hipError_t launch_rows(void (*kernel)(const Args, uint32_t, uint32_t, uint32_t, uint32_t), const Args& a, uint32_t rows,
+                       uint32_t rows_per_wave, hipStream_t stream) {
+    const uint32_t steps = (rows + rows_per_wave - 1u) / rows_per_wave;
+    const uint32_t iters = a.n_tok >= kManyTokens ? steps : 1u;
+    const uint32_t chunks = (steps + iters - 1u) / iters;
+    const uint32_t most = max((1u << 24) / chunks, 1u);
+    for (uint64_t base = 0; base < a.n_tok; base += most) {
+        const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(most), a.n_tok - base));
+        hipLaunchKernelGGL(kernel, dim3((n * chunks + 3u) / 4u), dim3(256), 0, stream, a, static_cast<uint32_t>(base),
+                           static_cast<uint32_t>(base) + n, chunks, iters);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <class T, int D>
+hipError_t norm_rope_one(const NormRopeArgs& a, hipStream_t stream) {
+    return launch_rows<NormRopeArgs>(norm_rope_kernel<T, D>, a, a.heads[0] + a.heads[1], 1024 / D, stream);
+}
+
+template <class T, int D, bool kE4m3>
+hipError_t append_one(const AppendArgs& a, hipStream_t stream) {
+    return launch_rows<AppendArgs>(append_kernel<T, D, kE4m3>, a, 2u * a.cache.n_kv_heads, 1024 / D, stream);
+}
+
+template <class T>
+hipError_t norm_rope_dim(const NormRopeArgs& a, uint32_t dim, hipStream_t stream) {
+    switch (dim) {
+        case 64: return norm_rope_one<T, 64>(a, stream);
+        case 128: return norm_rope_one<T, 128>(a, stream);
+        default: return norm_rope_one<T, 256>(a, stream);
+    }
+}
+
+template <class T, bool kE4m3>
+hipError_t append_dim(const AppendArgs& a, uint32_t dim, hipStream_t stream) {
+    switch (dim) {
+        case 64: return append_one<T, 64, kE4m3>(a, stream);
+        case 128: return append_one<T, 128, kE4m3>(a, stream);
+        default: return append_one<T, 256, kE4m3>(a, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_norm_rope(const NormRopeArgs& a, uint32_t dim, uint32_t type, hipStream_t stream) {
+    return type == ENGRAM_BF16 ? norm_rope_dim<Bf16>(a, dim, stream) : norm_rope_dim<F16>(a, dim, stream);
+}
+
+hipError_t launch_append(const AppendArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream) {
+    if (type == ENGRAM_BF16)
+        return e4m3 ? append_dim<Bf16, true>(a, dim, stream) : append_dim<Bf16, false>(a, dim, stream);
+    return e4m3 ? append_dim<F16, true>(a, dim, stream) : append_dim<F16, false>(a, dim, stream);
+}
+
+}  // namespace engram

@@ -1,0 +1,130 @@
+// Shared by the paged attention kernels: arguments, the rows of a request,
+// and how a launch finds them.
+//
+// The rows of a request and KV head are its (new token i, head g of the group)
+// pairs, row r = i * G + g: the G query heads that share a KV head read the
+// same keys, so a tile of rows reads each key once for all of them.  A row's
+// token sits at position p = kv_len - q_len + i and sees the keys
+// max(0, p - window + 1) .. p (window 0: all keys up to p).
+#pragma once
+
+#include "serving.h"
+
+namespace engram {
+
+struct AttentionArgs {
+    const uint8_t* q;
+    uint8_t* out;
+    float* lse;              // nullptr: not wanted
+    const int32_t* table;    // [n_seq][table_width], row stride table_stride
+    const int32_t* kv_len;   // [n_seq]
+    const int32_t* cu_q;     // [n_seq + 1], or nullptr: n_tok / n_seq tokens each
+    CacheView cache;
+    float* part_o;           // [n_split][n_tok][n_q_heads][dim] sums of a split, not divided
+    float* part_ml;          // [n_split][n_tok][n_q_heads][2] maximum (in units of log2) and sum
+    int64_t q_tok, q_head, out_tok, out_head;  // strides, elements
+    int64_t table_stride;
+    uint32_t table_width;
+    uint32_t n_seq;
+    uint32_t n_tok;
+    uint32_t uniform_q;      // tokens of each request where cu_q is nullptr
+    uint32_t group;          // query heads per KV head
+    uint32_t window;
+    uint32_t split_tokens;   // keys of a split; 0: one split takes all
+    uint32_t n_split;
+    uint32_t min_rows, max_rows;  // requests of this launch: min_rows <= rows <= max_rows
+    float scale_log2;        // scale * log2(e)
+};
+
+// One request as a launch sees it.  Lengths are bounded by what exists, so
+// that no value of cu_q or kv_len leads outside of the buffers.
+struct Request {
+    uint32_t q0, q_len;
+    int32_t kv_len;
+};
+
+__device__ __forceinline__ Request request_of(const AttentionArgs& A, uint32_t b) {
+    Request r;
+    if (A.cu_q) {
+        const int32_t n = static_cast<int32_t>(A.n_tok);
+        const int32_t q0 = min(max(A.cu_q[b], 0), n);
+        const int32_t q1 = min(max(A.cu_q[b + 1], q0), n);
+        r.q0 = static_cast<uint32_t>(q0);
+        r.q_len = static_cast<uint32_t>(q1 - q0);
+    } else {
+        r.q0 = b * A.uniform_q;
+        r.q_len = A.uniform_q;
+    }
+    const uint64_t room = static_cast<uint64_t>(A.table_width) << A.cache.page_shift;
+    const int32_t most = room < 0x7FFFFF00ull ? static_cast<int32_t>(room) : 0x7FFFFF00;
+    r.kv_len = min(max(A.kv_len[b], 0), most);
+    return r;
+}
+
+// Tiles of kRows rows over all requests.  With equal requests tile t is tile
+// t % per of request t / per.  With cu_q the tiles of request b start at
+// floor(cu_q[b] * G / kRows) + b, which leaves room for each request's last,
+// partly filled tile whatever the lengths are: floor(x + y) + 1 - floor(x)
+// >= ceil(y).  The wave finds b 64 candidates at a time.
+struct Tile {
+    uint32_t b, row0;
+    bool live;
+};
+
+template <uint32_t kRows>
+__device__ __forceinline__ uint32_t tile_start(const AttentionArgs& A, uint32_t b) {
+    const int32_t n = static_cast<int32_t>(A.n_tok);
+    const uint64_t rows = static_cast<uint64_t>(min(max(A.cu_q[b], 0), n)) * A.group;
+    return static_cast<uint32_t>(rows / kRows) + b;
+}
+
+template <uint32_t kRows>
+__device__ __forceinline__ Tile find_tile(const AttentionArgs& A, uint32_t t) {
+    Tile r;
+    if (!A.cu_q) {
+        const uint32_t per = (A.uniform_q * A.group + kRows - 1u) / kRows;
+        r.b = t / per;
+        r.row0 = (t - r.b * per) * kRows;
+        r.live = r.b < A.n_seq;
+        return r;
+    }
+    const uint32_t lane = threadIdx.x & 63u;
+    uint32_t lo = 0, n = A.n_seq;  // the last request of [lo, lo + n) that starts at or before t
+    while (n > 1u) {
+        const uint32_t step = (n + 63u) / 64u;
+        const uint32_t at = lo + lane * step;
+        const bool before = at < lo + n && tile_start<kRows>(A, at) <= t;
+        const uint32_t k = static_cast<uint32_t>(__builtin_popcountll(__ballot(before)));
+        const uint32_t first = k ? lo + (k - 1u) * step : lo;  // lane 0 holds in every ordered cu_q
+        n = min(step, lo + n - first);
+        lo = first;
+    }
+    r.b = lo;
+    r.row0 = (t - min(t, tile_start<kRows>(A, lo))) * kRows;
+    r.live = true;
+    return r;
+}
+
+template <uint32_t kRows>
+inline uint32_t tile_count(const AttentionArgs& A) {
+    if (!A.cu_q) return A.n_seq * ((A.uniform_q * A.group + kRows - 1u) / kRows);
+    return static_cast<uint32_t>(static_cast<uint64_t>(A.n_tok) * A.group / kRows) + A.n_seq;
+}
+
+// Keys that the rows [row0, row0 + n) of a request can see: [lo, hi).
+struct Span {
+    int32_t lo, hi;
+};
+__device__ __forceinline__ Span span_of(const AttentionArgs& A, const Request& r, uint32_t row0, uint32_t rows) {
+    const int32_t back = r.kv_len - static_cast<int32_t>(r.q_len);
+    const int32_t first = back + static_cast<int32_t>(row0 / A.group);
+    const int32_t last = back + static_cast<int32_t>((row0 + rows - 1u) / A.group);
+    Span s;
+    s.hi = last + 1;
+    s.lo = A.window && first >= static_cast<int32_t>(A.window) ? first - static_cast<int32_t>(A.window) + 1 : 0;
+    return s;
+}
+
+hipError_t launch_paged_rows(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
+
+}  // namespace engram

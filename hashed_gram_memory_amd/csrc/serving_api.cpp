@@ -1,0 +1,259 @@
+// Host side of the serving calls (head norm + rotation, cache append, paged
+// attention): validation, the split of the keys, launches.  As in
+// engram_api.cpp, every argument is checked before anything is launched and
+// nothing here synchronises or allocates device memory.
+#include <algorithm>
+#include <math.h>
+
+#include "engram_internal.h"
+#include "paged_attention.h"
+
+using namespace engram;
+
+namespace {
+
+bool good_dim(uint32_t d) { return d == 64 || d == 128 || d == 256; }
+bool good_type(uint32_t t) { return t == ENGRAM_BF16 || t == ENGRAM_F16; }
+
+// Strides of a [tokens][heads][dim] tensor: whole 16-byte blocks, not negative.
+bool good_strides(int64_t tok, int64_t head) {
+    constexpr int64_t kMost = int64_t(1) << 40;
+    return tok >= 0 && head >= 0 && tok < kMost && head < kMost && tok % 8 == 0 && head % 8 == 0;
+}
+
+int check_rotation(uint32_t rotary, uint32_t dim, int64_t n_tok, const int32_t* positions, const double* inv_freq,
+                   uint32_t interleaved, float eps) {
+    if (rotary % 16 != 0 || rotary > dim || interleaved > 1) return ENGRAM_EINVAL;
+    if (!(eps >= 0.0f) || isinf(eps)) return ENGRAM_EINVAL;
+    if (rotary && n_tok > 0 && (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 8)))
+        return ENGRAM_EINVAL;
+    return ENGRAM_OK;
+}
+
+int view_of(const engram_kv_cache* c, CacheView* out) {
+    if (!c) return ENGRAM_EINVAL;
+    if (c->type != ENGRAM_BF16 && c->type != ENGRAM_F16 && c->type != ENGRAM_E4M3) return ENGRAM_EUNSUPPORTED;
+    if (!good_dim(c->head_dim)) return ENGRAM_EUNSUPPORTED;
+    const uint32_t p = c->page_size;
+    if (p < 8 || p > 1024 || (p & (p - 1)) != 0) return ENGRAM_EUNSUPPORTED;
+    if (c->n_kv_heads == 0 || c->n_kv_heads > 65535 || c->n_pages <= 0 || c->n_pages > INT32_MAX) return ENGRAM_ERANGE;
+    if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return ENGRAM_EINVAL;
+    const int64_t inner = int64_t(c->n_kv_heads) * p * c->head_dim;
+    const int64_t most = INT64_MAX / 2 / c->n_pages;
+    for (int64_t s : {c->k_page_stride, c->v_page_stride})
+        if (s < inner || s % 16 != 0 || s > most) return ENGRAM_EINVAL;
+    if (c->type == ENGRAM_E4M3 &&
+        (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
+        return ENGRAM_EINVAL;
+    out->k = static_cast<uint8_t*>(c->k);
+    out->v = static_cast<uint8_t*>(c->v);
+    out->k_scale = c->k_scale;
+    out->v_scale = c->v_scale;
+    out->k_page_stride = c->k_page_stride;
+    out->v_page_stride = c->v_page_stride;
+    out->n_pages = c->n_pages;
+    out->n_kv_heads = c->n_kv_heads;
+    out->page_shift = static_cast<uint32_t>(__builtin_ctz(p));
+    return ENGRAM_OK;
+}
+
+// How a call's keys are divided and which kernels take its rows.
+struct Choice {
+    uint32_t split_tokens, n_split;
+};
+
+// Keys of a split.  A workgroup takes 128 keys at a time, and the chip needs
+// several workgroups on each of its 256 CUs; the keys of a tile are halved
+// until there are that many, or a split is 256 keys long.
+Choice choose(uint64_t groups, int64_t most_keys) {
+    constexpr uint64_t kEnough = 2048;
+    constexpr int64_t kLeast = 256;
+    int64_t split = kLeast;
+    while (split < most_keys && groups * static_cast<uint64_t>((most_keys + 2 * split - 1) / (2 * split)) >= kEnough)
+        split *= 2;
+    while ((most_keys + split - 1) / split > 1024) split *= 2;
+    Choice c;
+    c.n_split = static_cast<uint32_t>(std::max<int64_t>(1, (most_keys + split - 1) / split));
+    c.split_tokens = c.n_split > 1 ? static_cast<uint32_t>(split) : 0u;
+    return c;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Checks a description and fills the kernels' arguments (without the workspace).
+int attention_args(const engram_attention_desc* d, AttentionArgs* a, size_t* ws_bytes) {
+    if (!d) return ENGRAM_EINVAL;
+    CacheView view;
+    const int st = view_of(d->cache, &view);
+    if (st != ENGRAM_OK) return st;
+    if (!good_type(d->type)) return ENGRAM_EUNSUPPORTED;
+    if (d->cache->type != ENGRAM_E4M3 && d->cache->type != d->type) return ENGRAM_EUNSUPPORTED;
+    if (d->n_seq < 0 || d->n_tok < 0 || d->table_width < 0 || d->max_q_len < 0 || d->window < 0) return ENGRAM_EINVAL;
+    if (d->n_q_heads == 0 || d->n_q_heads > 65535 || d->n_q_heads % d->cache->n_kv_heads != 0) return ENGRAM_EINVAL;
+    if (d->reserved0 != 0) return ENGRAM_EINVAL;
+    if (d->n_tok > INT32_MAX / int64_t(d->n_q_heads) || d->n_seq > (1 << 24) || d->window > INT32_MAX ||
+        d->table_width > INT32_MAX)
+        return ENGRAM_ERANGE;
+    *ws_bytes = 0;
+    if (d->n_tok == 0) return ENGRAM_OK;
+    if (d->n_seq == 0) return ENGRAM_EINVAL;
+    if (!d->cu_q && d->n_tok % d->n_seq != 0) return ENGRAM_EINVAL;
+    if (!isfinite(d->scale)) return ENGRAM_EINVAL;
+    if (!d->q || !d->out || !d->kv_len || !aligned(d->q, 16) || !aligned(d->out, 16) || !aligned(d->kv_len, 4) ||
+        !aligned(d->cu_q, 4) || !aligned(d->lse, 4))
+        return ENGRAM_EINVAL;
+    if (d->table_width > 0 && (!d->block_table || !aligned(d->block_table, 4) || d->table_stride < d->table_width))
+        return ENGRAM_EINVAL;
+    if (d->table_stride < 0 || d->table_stride > (int64_t(1) << 40)) return ENGRAM_EINVAL;
+    if (!good_strides(d->q_token_stride, d->q_head_stride) || !good_strides(d->out_token_stride, d->out_head_stride))
+        return ENGRAM_EINVAL;
+
+    a->q = static_cast<const uint8_t*>(d->q);
+    a->out = static_cast<uint8_t*>(d->out);
+    a->lse = d->lse;
+    a->table = d->block_table;
+    a->kv_len = d->kv_len;
+    a->cu_q = d->cu_q;
+    a->cache = view;
+    a->part_o = nullptr;
+    a->part_ml = nullptr;
+    a->q_tok = d->q_token_stride;
+    a->q_head = d->q_head_stride;
+    a->out_tok = d->out_token_stride;
+    a->out_head = d->out_head_stride;
+    a->table_stride = d->table_stride;
+    a->table_width = static_cast<uint32_t>(d->table_width);
+    a->n_seq = static_cast<uint32_t>(d->n_seq);
+    a->n_tok = static_cast<uint32_t>(d->n_tok);
+    a->uniform_q = d->cu_q ? 0u : static_cast<uint32_t>(d->n_tok / d->n_seq);
+    a->group = d->n_q_heads / view.n_kv_heads;
+    a->window = static_cast<uint32_t>(d->window);
+    a->scale_log2 = d->scale * 1.4426950408889634f;
+    a->min_rows = 0;
+    a->max_rows = UINT32_MAX;
+
+    const uint64_t tiles = tile_count<16>(*a);
+    if (tiles * view.n_kv_heads > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
+    int64_t most_keys = std::min<int64_t>(d->table_width << view.page_shift, INT32_MAX - 255);
+    // a window bounds the keys of a tile: its own, those of its other tokens, and the step it begins in
+    if (d->window) most_keys = std::min<int64_t>(most_keys, d->window + 16 + 32);
+    const Choice c = choose(tiles * view.n_kv_heads, most_keys);
+    a->split_tokens = c.split_tokens;
+    a->n_split = c.n_split;
+    if (c.n_split > 1) {
+        const size_t rows = size_t(c.n_split) * a->n_tok * d->n_q_heads;
+        *ws_bytes = up256(rows * d->cache->head_dim * 4) + up256(rows * 8);
+    }
+    return ENGRAM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int engram_qk_norm_rope(const engram_norm_rope_desc* d, void* stream) {
+    if (!d) return ENGRAM_EINVAL;
+    if (!good_type(d->type) || !good_dim(d->head_dim)) return ENGRAM_EUNSUPPORTED;
+    if (d->n_tok < 0 || d->reserved0 != 0) return ENGRAM_EINVAL;
+    if (d->n_tok > kMaxTokens || d->n_q_heads > 65535 || d->n_k_heads > 65535) return ENGRAM_ERANGE;
+    int st = check_rotation(d->rotary_dim, d->head_dim, d->n_tok, d->positions, d->inv_freq, d->interleaved, d->eps);
+    if (st != ENGRAM_OK) return st;
+    NormRopeArgs a;
+    const struct {
+        const void *src, *dst, *weight;
+        uint32_t heads;
+        int64_t st, sh, dt, dh;
+    } side[2] = {{d->q, d->q_out, d->q_weight, d->n_q_heads, d->q_token_stride, d->q_head_stride, d->q_out_token_stride,
+                  d->q_out_head_stride},
+                 {d->k, d->k_out, d->k_weight, d->n_k_heads, d->k_token_stride, d->k_head_stride, d->k_out_token_stride,
+                  d->k_out_head_stride}};
+    for (int i = 0; i < 2; ++i) {
+        const auto& s = side[i];
+        if (s.heads && d->n_tok) {
+            if (!s.src || !s.dst || !aligned(s.src, 16) || !aligned(s.dst, 16) || !aligned(s.weight, 16))
+                return ENGRAM_EINVAL;
+            if (!good_strides(s.st, s.sh) || !good_strides(s.dt, s.dh)) return ENGRAM_EINVAL;
+        }
+        a.src[i] = static_cast<const uint8_t*>(s.src);
+        a.dst[i] = static_cast<uint8_t*>(const_cast<void*>(s.dst));
+        a.weight[i] = static_cast<const uint8_t*>(s.weight);
+        a.heads[i] = s.heads;
+        a.src_tok[i] = s.st;
+        a.src_head[i] = s.sh;
+        a.dst_tok[i] = s.dt;
+        a.dst_head[i] = s.dh;
+    }
+    if (d->n_tok == 0 || d->n_q_heads + d->n_k_heads == 0) return ENGRAM_OK;
+    a.positions = d->positions;
+    a.inv_freq = d->inv_freq;
+    a.n_tok = static_cast<uint32_t>(d->n_tok);
+    a.rotary = d->rotary_dim;
+    a.interleaved = d->interleaved;
+    a.eps = d->eps;
+    const hipError_t e = launch_norm_rope(a, d->head_dim, d->type, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
+}
+
+int engram_kv_append(const engram_append_desc* d, void* stream) {
+    if (!d) return ENGRAM_EINVAL;
+    AppendArgs a;
+    int st = view_of(d->cache, &a.cache);
+    if (st != ENGRAM_OK) return st;
+    if (!good_type(d->type)) return ENGRAM_EUNSUPPORTED;
+    if (d->cache->type != ENGRAM_E4M3 && d->cache->type != d->type) return ENGRAM_EUNSUPPORTED;
+    if (d->n_tok < 0 || d->reserved0 != 0) return ENGRAM_EINVAL;
+    if (d->n_tok > kMaxTokens) return ENGRAM_ERANGE;
+    st = check_rotation(d->rotary_dim, d->cache->head_dim, d->n_tok, d->positions, d->inv_freq, d->interleaved, d->eps);
+    if (st != ENGRAM_OK) return st;
+    if (d->n_tok == 0) return ENGRAM_OK;
+    if (!d->k || !d->v || !d->slots || !aligned(d->k, 16) || !aligned(d->v, 16) || !aligned(d->slots, 8) ||
+        !aligned(d->k_weight, 16))
+        return ENGRAM_EINVAL;
+    if (!good_strides(d->k_token_stride, d->k_head_stride) || !good_strides(d->v_token_stride, d->v_head_stride))
+        return ENGRAM_EINVAL;
+    a.src[0] = static_cast<const uint8_t*>(d->k);
+    a.src[1] = static_cast<const uint8_t*>(d->v);
+    a.src_tok[0] = d->k_token_stride;
+    a.src_head[0] = d->k_head_stride;
+    a.src_tok[1] = d->v_token_stride;
+    a.src_head[1] = d->v_head_stride;
+    a.weight = static_cast<const uint8_t*>(d->k_weight);
+    a.positions = d->positions;
+    a.inv_freq = d->inv_freq;
+    a.slots = d->slots;
+    a.n_tok = static_cast<uint32_t>(d->n_tok);
+    a.rotary = d->rotary_dim;
+    a.interleaved = d->interleaved;
+    a.eps = d->eps;
+    const hipError_t e = launch_append(a, d->cache->head_dim, d->type, d->cache->type == ENGRAM_E4M3,
+                                       static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
+}
+
+int engram_paged_attention_workspace(const engram_attention_desc* d, size_t* bytes) {
+    if (!bytes) return ENGRAM_EINVAL;
+    AttentionArgs a;
+    size_t need = 0;
+    const int st = attention_args(d, &a, &need);
+    if (st == ENGRAM_OK) *bytes = need;
+    return st;
+}
+
+int engram_paged_attention(const engram_attention_desc* d, void* ws, size_t ws_bytes, void* stream) {
+    AttentionArgs a;
+    size_t need = 0;
+    const int st = attention_args(d, &a, &need);
+    if (st != ENGRAM_OK) return st;
+    if (d->n_tok == 0) return ENGRAM_OK;
+    if (need) {
+        if (!ws || ws_bytes < need || !aligned(ws, 256)) return ENGRAM_EWORKSPACE;
+        const size_t rows = size_t(a.n_split) * a.n_tok * d->n_q_heads;
+        a.part_o = static_cast<float*>(ws);
+        a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + up256(rows * d->cache->head_dim * 4));
+    }
+    const hipError_t e = launch_paged_rows(a, d->cache->head_dim, d->type, d->cache->type == ENGRAM_E4M3,
+                                           static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
+}
+
+}  // extern "C"

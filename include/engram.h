@@ -405,6 +405,192 @@ int engram_dedup_noalloc(engram_plan_t plan, const int32_t* ids, const int32_t* 
                          int64_t n_seq, int64_t seq_len, int32_t* perm, int32_t* offsets,
                          int32_t* n_unique, void* stream);
 
+/*
+ * Serving operators: the attention layer that reads the same tokens as the
+ * lookup.  With the tables resident, the rest of a GPU's memory is the
+ * requests' KV cache [VRAM; GUIDE "Where the 510 GB goes"]; these calls norm
+ * and rotate the heads of new tokens, append keys and values to a paged cache
+ * and attend over it.  They use no plan.  Conventions as above; descriptions
+ * are host structures read during the call, and every reserved field must
+ * be 0.  q, k, v and out are [n_tok][heads][head_dim] with any token and head
+ * stride (elements, multiples of 8, not negative) and 16-byte aligned, so
+ * that the slices of one projection's output can be passed as they are.
+ */
+
+/* Element types.  E4M3 (OCP) only as a cache's type. */
+#define ENGRAM_BF16 0
+#define ENGRAM_F16 1
+#define ENGRAM_E4M3 2
+
+/*
+ * A paged cache: K and V each [n_pages][n_kv_heads][page_size][head_dim] of
+ * `type`; pages are k_page_stride and v_page_stride elements apart (multiples
+ * of 16, at least one page's size; K and V may be halves of one allocation).
+ * An ENGRAM_E4M3 cache holds FP8 codes and one fp32 scale for each (page,
+ * head, slot), k_scale and v_scale [n_pages][n_kv_heads][page_size]: a row
+ * stands for codes * scale, as a table row does.
+ *
+ *   page_size   a power of two from 8 to 1024; head_dim 64, 128 or 256;
+ *               n_kv_heads 1 to 65535; n_pages 1 to 2^31 - 1.
+ * All pointers 16-byte aligned.
+ */
+typedef struct engram_kv_cache {
+    void* k;
+    void* v;
+    float* k_scale;               /* NULL unless ENGRAM_E4M3 */
+    float* v_scale;
+    int64_t k_page_stride;
+    int64_t v_page_stride;
+    int64_t n_pages;
+    uint32_t n_kv_heads;
+    uint32_t page_size;
+    uint32_t head_dim;
+    uint32_t type;
+} engram_kv_cache;
+
+/*
+ * Norm and rotation of query and key heads, in one pass:
+ *     y = x * rsqrt(mean(x^2) + eps) * weight        (no weight: y = x)
+ *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
+ *     t = positions[tok] * inv_freq[i], i = 0 .. rotary_dim/2 - 1,
+ * (a, b) = (i, i + rotary_dim/2), or (2i, 2i + 1) with interleaved = 1;
+ * elements from rotary_dim on are not rotated.  fp32 arithmetic (angles in
+ * fp64), rounded once to `type`.  An output may be its input (same strides);
+ * otherwise they must not overlap.
+ *
+ *   head_dim    64, 128 or 256.  rotary_dim: a multiple of 16, at most
+ *               head_dim; 0 for none (positions and inv_freq may be NULL).
+ *   n_q_heads, n_k_heads   0 to 65535; 0 leaves that side out.
+ *   q_weight, k_weight     device [head_dim] of `type`, 16-byte aligned, or NULL.
+ *   positions   device int32 [n_tok], any value.
+ *   inv_freq    device double [rotary_dim / 2].
+ *
+ * n_tok == 0 is a no-op.  Errors: EINVAL, ERANGE (n_tok > 2^31 - 1, a head
+ * count above 65535), EUNSUPPORTED (type, head_dim).
+ */
+typedef struct engram_norm_rope_desc {
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    const void* q_weight;
+    const void* k_weight;
+    const int32_t* positions;
+    const double* inv_freq;
+    int64_t n_tok;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride;
+    int64_t k_out_token_stride, k_out_head_stride;
+    uint32_t n_q_heads, n_k_heads;
+    uint32_t head_dim;
+    uint32_t rotary_dim;
+    uint32_t interleaved;
+    uint32_t type;
+    float eps;
+    uint32_t reserved0;
+} engram_norm_rope_desc;
+
+int engram_qk_norm_rope(const engram_norm_rope_desc* desc, void* stream);
+
+/*
+ * Append new keys and values to a paged cache.  The key of token i (normed
+ * if k_weight is given, rotated if rotary_dim > 0, both as above) and its
+ * value go to page slots[i] / page_size, place slots[i] % page_size.  A
+ * negative slot, or one past the pool, writes nothing (a batch's padding).
+ * Two tokens of one call must not name the same slot.
+ *   type of k, v and the cache: equal, or an ENGRAM_E4M3 cache, where each
+ * row x is stored as scale = max|x| / 448 and the codes nearest to
+ * x * 448 / max|x| (ties to even); a row of zeros has scale 0, and a NaN in
+ * a row makes its scale NaN.  Nothing but the named rows (and their scales) is
+ * written.
+ *
+ *   slots       device int64 [n_tok], 8-byte aligned.
+ *
+ * n_tok == 0 is a no-op.  Errors: EINVAL, ERANGE, EUNSUPPORTED (a type or
+ * geometry other than the above).
+ */
+typedef struct engram_append_desc {
+    const engram_kv_cache* cache;
+    const void* k;
+    const void* v;
+    const void* k_weight;
+    const int32_t* positions;
+    const double* inv_freq;
+    const int64_t* slots;
+    int64_t n_tok;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    uint32_t rotary_dim;
+    uint32_t interleaved;
+    uint32_t type;
+    float eps;
+    uint32_t reserved0;
+    uint32_t reserved1;
+} engram_append_desc;
+
+int engram_kv_append(const engram_append_desc* desc, void* stream);
+
+/*
+ * Attention of new tokens over a paged cache that already holds them.
+ * Request b has the q_len tokens cu_q[b] .. cu_q[b + 1] - 1 of q (cu_q NULL:
+ * n_tok / n_seq each) and kv_len[b] cached keys; key j lies on page
+ * block_table[b][j / page_size], place j % page_size.  Its token i is at
+ * position p = kv_len[b] - q_len + i and sees the keys j <= p, with a window
+ * w > 0 those with j > p - w.  Query head h reads KV head
+ * h / (n_q_heads / n_kv_heads):
+ *     out = sum_j a_j v_j / sum_j a_j,  a_j = exp(scale * q . k_j - max),
+ *     lse = log(sum_j exp(scale * q . k_j))            (natural)
+ * A token that sees no key gets out = 0 and lse = -infinity.  What a token
+ * does not see never reaches its result, NaN and infinities included.
+ * Products of 16-bit operands with fp32 sums; softmax in fp32.
+ *
+ *   lse         device fp32 [n_tok][n_q_heads], or NULL.
+ *   block_table device int32 [n_seq][table_width], rows table_stride apart.  A
+ *               page number outside the pool is never read: its keys count
+ *               as unseen.  kv_len is bounded by table_width * page_size and
+ *               by 0; entries past a request's last page are not read.
+ *   max_q_len   a bound of the requests' q_len where cu_q is given, 0 if not
+ *               known.  It decides which kernels run, not what they compute.
+ *   window      0 for none.
+ *   scale       finite.
+ *   cu_q        device int32 [n_seq + 1], ascending from 0 to n_tok.  Values
+ *               that are not leave results unspecified; nothing out of bounds
+ *               is read or written.
+ *   ws          device workspace of engram_paged_attention_workspace bytes
+ *               (host-only; 0 for few keys), 256-byte aligned.  It holds
+ *               nothing between calls; one call at a time may use it.
+ *
+ * Results are the same on every call with the same arguments.  n_tok == 0
+ * is a no-op.  Errors: EINVAL, ERANGE (n_tok * n_q_heads > 2^31 - 1, or
+ * n_tok * n_q_heads / 16 + n_seq * n_kv_heads > 2^23: split the batch),
+ * EUNSUPPORTED, EWORKSPACE.
+ */
+typedef struct engram_attention_desc {
+    const engram_kv_cache* cache;
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* block_table;
+    const int32_t* kv_len;
+    const int32_t* cu_q;
+    int64_t n_seq;
+    int64_t n_tok;
+    int64_t max_q_len;
+    int64_t table_width;
+    int64_t table_stride;
+    int64_t window;
+    int64_t q_token_stride, q_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    uint32_t n_q_heads;
+    uint32_t type;
+    float scale;
+    uint32_t reserved0;
+} engram_attention_desc;
+
+int engram_paged_attention_workspace(const engram_attention_desc* desc, size_t* bytes);
+int engram_paged_attention(const engram_attention_desc* desc, void* ws, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* engram_status_string(int status);
 
