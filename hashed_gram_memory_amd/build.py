@@ -21,7 +21,8 @@ DEMO_SRC = os.path.join(CSRC, "examples", "c_abi_demo.c")
 DEMO = os.path.join(HERE, "c_abi_demo")
 # the lookup library (the product) and the measurement library (synthetic table fill, memory-ceiling probes)
 SOURCES = ["engram_api.cpp", "hash.hip", "gather_reduce.hip", "dedup.hip", "lookup.hip", "gate_io.hip",
-           "gather_batched.hip", "dedup_noalloc.hip", "check.hip", "serving_api.cpp", "norm_rope.hip", "paged_rows.hip"]
+           "gather_batched.hip", "dedup_noalloc.hip", "check.hip", "serving_api.cpp", "norm_rope.hip", "paged_rows.hip",
+           "paged_tile.hip", "paged_join.hip"]
 MEASURE_SOURCES = ["synth_fill.hip", "probe.hip"]
 MEASURE_LIB = os.path.join(HERE, "libengram_measure.so")
 ARCH = "gfx950"

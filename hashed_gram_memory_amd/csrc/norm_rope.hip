@@ -20,6 +20,8 @@
 // the interleaved form each block holds its own pairs.  Either way a lane
 // needs 8 cosines and sines, computed once and used for every row that the
 // wave takes of its token.
+#include <algorithm>
+
 #include "serving.h"
 
 namespace engram {
@@ -258,9 +260,9 @@ hipError_t launch_rows(void (*kernel)(const Args, uint32_t, uint32_t, uint32_t, 
     const uint32_t steps = (rows + rows_per_wave - 1u) / rows_per_wave;
     const uint32_t iters = a.n_tok >= kManyTokens ? steps : 1u;
     const uint32_t chunks = (steps + iters - 1u) / iters;
-    const uint32_t most = max((1u << 24) / chunks, 1u);
+    const uint32_t most = std::max((1u << 24) / chunks, 1u);
     for (uint64_t base = 0; base < a.n_tok; base += most) {
-        const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(most), a.n_tok - base));
+        const uint32_t n = static_cast<uint32_t>(std::min<uint64_t>(most, a.n_tok - base));
         hipLaunchKernelGGL(kernel, dim3((n * chunks + 3u) / 4u), dim3(256), 0, stream, a, static_cast<uint32_t>(base),
                            static_cast<uint32_t>(base) + n, chunks, iters);
         const hipError_t e = hipGetLastError();

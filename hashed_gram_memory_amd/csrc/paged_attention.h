@@ -20,8 +20,8 @@ struct AttentionArgs {
     const int32_t* kv_len;   // [n_seq]
     const int32_t* cu_q;     // [n_seq + 1], or nullptr: n_tok / n_seq tokens each
     CacheView cache;
-    float* part_o;           // [n_split][n_tok][n_q_heads][dim] sums of a split, not divided
-    float* part_ml;          // [n_split][n_tok][n_q_heads][2] maximum (in units of log2) and sum
+    float* part_o;           // [n_split][rows][dim] sums of a split, not divided (rows: part_index)
+    float* part_ml;          // [n_split][rows][2] maximum (in units of log2) and sum
     int64_t q_tok, q_head, out_tok, out_head;  // strides, elements
     int64_t table_stride;
     uint32_t table_width;
@@ -33,6 +33,7 @@ struct AttentionArgs {
     uint32_t split_tokens;   // keys of a split; 0: one split takes all
     uint32_t n_split;
     uint32_t min_rows, max_rows;  // requests of this launch: min_rows <= rows <= max_rows
+    uint32_t tiles_per;      // tiles set aside for each request; 0: as the lengths need (find_tile)
     float scale_log2;        // scale * log2(e)
 };
 
@@ -61,8 +62,9 @@ __device__ __forceinline__ Request request_of(const AttentionArgs& A, uint32_t b
     return r;
 }
 
-// Tiles of kRows rows over all requests.  With equal requests tile t is tile
-// t % per of request t / per.  With cu_q the tiles of request b start at
+// Tiles of kRows rows over all requests.  With equal requests, or where a bound
+// of their lengths is small, tile t is tile t % tiles_per of request
+// t / tiles_per.  Else (cu_q) the tiles of request b start at
 // floor(cu_q[b] * G / kRows) + b, which leaves room for each request's last,
 // partly filled tile whatever the lengths are: floor(x + y) + 1 - floor(x)
 // >= ceil(y).  The wave finds b 64 candidates at a time.
@@ -81,10 +83,9 @@ __device__ __forceinline__ uint32_t tile_start(const AttentionArgs& A, uint32_t 
 template <uint32_t kRows>
 __device__ __forceinline__ Tile find_tile(const AttentionArgs& A, uint32_t t) {
     Tile r;
-    if (!A.cu_q) {
-        const uint32_t per = (A.uniform_q * A.group + kRows - 1u) / kRows;
-        r.b = t / per;
-        r.row0 = (t - r.b * per) * kRows;
+    if (A.tiles_per) {
+        r.b = t / A.tiles_per;
+        r.row0 = (t - r.b * A.tiles_per) * kRows;
         r.live = r.b < A.n_seq;
         return r;
     }
@@ -107,7 +108,7 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& A, uint32_t t) {
 
 template <uint32_t kRows>
 inline uint32_t tile_count(const AttentionArgs& A) {
-    if (!A.cu_q) return A.n_seq * ((A.uniform_q * A.group + kRows - 1u) / kRows);
+    if (A.tiles_per) return A.n_seq * A.tiles_per;
     return static_cast<uint32_t>(static_cast<uint64_t>(A.n_tok) * A.group / kRows) + A.n_seq;
 }
 
@@ -125,6 +126,24 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& A, const Request& r
     return s;
 }
 
+// Where a divided row's parts lie.  Requests of few rows (max_rows) have that
+// many places each, so that their splits, which are many, need no room for the
+// rows of the long requests of the same call; the others lie by token and head.
+__device__ __forceinline__ uint64_t part_index(const AttentionArgs& A, uint32_t split, uint32_t b, uint32_t h,
+                                               uint32_t row, uint64_t flat) {
+    const uint64_t heads = A.cache.n_kv_heads;
+    if (A.max_rows != UINT32_MAX) return ((static_cast<uint64_t>(split) * A.n_seq + b) * heads + h) * A.max_rows + row;
+    return static_cast<uint64_t>(split) * A.n_tok * (heads * A.group) + flat;
+}
+
+constexpr uint32_t kRowsTile = 16;   // rows of a tile in paged_rows.hip
+constexpr uint32_t kTileRows = 256;  // and in paged_tile.hip
+// A split's keys begin at a multiple of this many: the keys of a step.
+constexpr int32_t kRowsAlign = 32, kTileAlign = 64;
+
 hipError_t launch_paged_rows(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
+hipError_t launch_paged_tile(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
+// Joins the parts that a launch of either wrote (many: paged_tile.hip's).
+hipError_t launch_paged_join(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, bool many, hipStream_t stream);
 
 }  // namespace engram

@@ -36,7 +36,7 @@
 namespace engram {
 namespace {
 
-constexpr uint32_t kRows = 16;
+constexpr uint32_t kRows = kRowsTile;
 constexpr uint32_t kStep = 32;      // keys of a wave's step
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kPages = 1024;   // page numbers held in LDS at a time
@@ -88,8 +88,8 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(const AttentionArgs A) 
     const Span span = span_of(A, req, tile.row0, n_rows);
     const Span first_row = span_of(A, req, tile.row0, 1), last_row = span_of(A, req, tile.row0 + n_rows - 1u, 1);
 
-    // this split's keys [c0, c1), from a multiple of 32
-    const int32_t base0 = span.lo & ~31;
+    // this split's keys [c0, c1)
+    const int32_t base0 = span.lo & ~(kRowsAlign - 1);
     const uint32_t split = blockIdx.y;
     const bool divided = A.split_tokens != 0 && span.hi > base0 &&
                          static_cast<uint32_t>(span.hi - base0) > A.split_tokens;
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(const AttentionArgs A) 
     const uint32_t out_tok = req.q0 + rr / A.group, out_head = h * A.group + rr % A.group;
     const uint64_t flat = static_cast<uint64_t>(out_tok) * (heads * A.group) + out_head;
     if (divided) {
-        const uint64_t at = static_cast<uint64_t>(split) * A.n_tok * (heads * A.group) + flat;
+        const uint64_t at = part_index(A, split, tile.b, h, rr, flat);
         float* dst = A.part_o + at * D + part * EPL;
 #pragma unroll
         for (int e = 0; e < EPL; e += 4)
@@ -391,84 +391,10 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(const AttentionArgs A) 
     if (A.lse && part == 0) A.lse[flat] = sum == 0.0f ? -INFINITY : (top + __log2f(sum) - P::kShift) * 0.69314718055994531f;
 }
 
-// The splits of a row joined, in their order: one workgroup for each row of a
-// tile and KV head.  kTile is the tile of the kernel that wrote the parts.
-template <class T, int D, bool kE4m3, uint32_t kTile>
-__global__ __launch_bounds__(256) void paged_join_kernel(const AttentionArgs A) {
-    constexpr int E = D / 64;  // channels of a lane
-    using P = std::conditional_t<kE4m3, Bf16, T>;
-    __shared__ float sm_o[4][D];
-    __shared__ float sm_m[4], sm_l[4];
-    const uint32_t heads = A.cache.n_kv_heads;
-    const uint32_t tile_at = blockIdx.x / heads, h = blockIdx.x - tile_at * heads;
-    const Tile tile = find_tile<kTile>(A, tile_at);
-    if (!tile.live) return;
-    const Request req = request_of(A, tile.b);
-    const uint32_t rows = req.q_len * A.group;
-    if (tile.row0 >= rows || rows < A.min_rows || rows > A.max_rows) return;
-    const uint32_t n_rows = min(kTile, rows - tile.row0);
-    if (blockIdx.y >= n_rows) return;
-    const Span span = span_of(A, req, tile.row0, n_rows);
-    const int32_t base0 = span.lo & ~31;
-    if (span.hi <= base0 || static_cast<uint32_t>(span.hi - base0) <= A.split_tokens) return;  // written whole
-    const uint32_t n_split = (static_cast<uint32_t>(span.hi - base0) + A.split_tokens - 1u) / A.split_tokens;
-
-    const uint32_t row = tile.row0 + blockIdx.y;
-    const uint32_t tok = req.q0 + row / A.group, head = h * A.group + row % A.group;
-    const uint64_t flat = static_cast<uint64_t>(tok) * (heads * A.group) + head;
-    const uint64_t step = static_cast<uint64_t>(A.n_tok) * (heads * A.group);
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
-
-    float m = -INFINITY, l = 0.0f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (uint32_t s = wave; s < n_split; s += 4u) {
-        const uint64_t at = s * step + flat;
-        const f32x2v ml = *reinterpret_cast<const f32x2v*>(A.part_ml + at * 2);
-        const float top = fmaxf(m, ml[0]);
-        const float ref = top == -INFINITY ? 0.0f : top;
-        const float a = __builtin_amdgcn_exp2f(m - ref), b = __builtin_amdgcn_exp2f(ml[0] - ref);
-        l = l * a + ml[1] * b;
-        m = top;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + A.part_o[at * D + lane * E + e] * b;
-    }
-    if (lane == 0) {
-        sm_m[wave] = m;
-        sm_l[wave] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[wave][lane * E + e] = acc[e];
-    __syncthreads();
-    if (wave != 0) return;
-    const float top = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sm_m[w] - ref);
-        sum += f * sm_l[w];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * sm_o[w][lane * E + e];
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t* dst = reinterpret_cast<uint16_t*>(A.out) + tok * A.out_tok + head * A.out_head + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[e] = static_cast<uint16_t>(T::pack(acc[e] * inv, 0.0f));
-    if (A.lse && lane == 0) A.lse[flat] = sum == 0.0f ? -INFINITY : (top + __log2f(sum) - P::kShift) * 0.69314718055994531f;
-}
-
 template <class T, int D, bool kE4m3>
 hipError_t rows_one(const AttentionArgs& a, hipStream_t stream) {
-    const uint32_t tiles = tile_count<kRows>(a);
-    const dim3 grid(tiles * a.cache.n_kv_heads, a.n_split);
+    const dim3 grid(tile_count<kRows>(a) * a.cache.n_kv_heads, a.n_split);
     hipLaunchKernelGGL((paged_rows_kernel<T, D, kE4m3>), grid, dim3(256), 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.n_split <= 1) return e;
-    const uint32_t most = a.cu_q ? kRows : min(kRows, a.uniform_q * a.group);
-    hipLaunchKernelGGL((paged_join_kernel<T, D, kE4m3, kRows>), dim3(tiles * a.cache.n_kv_heads, most), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -57,31 +57,60 @@ int view_of(const engram_kv_cache* c, CacheView* out) {
     return ENGRAM_OK;
 }
 
-// How a call's keys are divided and which kernels take its rows.
-struct Choice {
-    uint32_t split_tokens, n_split;
+// How one launch divides its keys.
+struct Split {
+    uint32_t tokens, n;  // keys of a split (0: all), splits
 };
 
-// Keys of a split.  A workgroup takes 128 keys at a time, and the chip needs
-// several workgroups on each of its 256 CUs; the keys of a tile are halved
-// until there are that many, or a split is 256 keys long.
-Choice choose(uint64_t groups, int64_t most_keys) {
+// Few rows (paged_rows.hip).  A workgroup takes 128 keys at a time, and the
+// chip needs several workgroups on each of its 256 CUs; the keys of a tile are
+// halved until there are that many, or a split is 256 keys long.
+Split split_rows(uint64_t groups, int64_t most_keys) {
     constexpr uint64_t kEnough = 2048;
     constexpr int64_t kLeast = 256;
     int64_t split = kLeast;
     while (split < most_keys && groups * static_cast<uint64_t>((most_keys + 2 * split - 1) / (2 * split)) >= kEnough)
         split *= 2;
     while ((most_keys + split - 1) / split > 1024) split *= 2;
-    Choice c;
-    c.n_split = static_cast<uint32_t>(std::max<int64_t>(1, (most_keys + split - 1) / split));
-    c.split_tokens = c.n_split > 1 ? static_cast<uint32_t>(split) : 0u;
-    return c;
+    const uint32_t n = static_cast<uint32_t>(std::max<int64_t>(1, (most_keys + split - 1) / split));
+    return {n > 1 ? static_cast<uint32_t>(split) : 0u, n};
+}
+
+// Many rows (paged_tile.hip).  A workgroup fills a CU, so a launch takes
+// ceil(groups * n / 256) rounds of a split's keys, and joining writes and reads
+// n fp32 rows for each row; of up to 32 splits the one with the least of both.
+Split split_tiles(uint64_t groups, int64_t most_keys, uint64_t rows, uint32_t dim) {
+    const double key_us = 4e-4 * dim, join_us = rows * dim * 8.0 / 4e6;
+    double best = 0;
+    Split s = {0u, 1u};
+    for (uint32_t n = 1; n <= 32; ++n) {
+        const int64_t tokens = ((most_keys + n - 1) / n + 63) / 64 * 64;
+        if (n > 1 && tokens < 256) break;
+        const double us = (groups * n + 255) / 256 * tokens * key_us + (n > 1 ? 6 + n * join_us : 0);
+        if (n == 1 || us < best) {
+            best = us;
+            s = {n > 1 ? static_cast<uint32_t>(tokens) : 0u, static_cast<uint32_t>((most_keys + tokens - 1) / tokens)};
+        }
+    }
+    if (s.n <= 1) s = {0u, 1u};
+    return s;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Rows of a request and KV head up to which paged_rows.hip takes it.
+constexpr uint32_t kFewRows = 64;
+
+// A call's launches: the requests of few rows, those of many, or both.
+struct Launches {
+    AttentionArgs few, many;
+    bool any_few, any_many;
+    size_t few_o, few_ml, many_o, many_ml;  // bytes of their parts
+};
+
 // Checks a description and fills the kernels' arguments (without the workspace).
-int attention_args(const engram_attention_desc* d, AttentionArgs* a, size_t* ws_bytes) {
+int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_bytes) {
+    AttentionArgs* const a = &out->few;
     if (!d) return ENGRAM_EINVAL;
     CacheView view;
     const int st = view_of(d->cache, &view);
@@ -131,19 +160,59 @@ int attention_args(const engram_attention_desc* d, AttentionArgs* a, size_t* ws_
     a->scale_log2 = d->scale * 1.4426950408889634f;
     a->min_rows = 0;
     a->max_rows = UINT32_MAX;
-
-    const uint64_t tiles = tile_count<16>(*a);
-    if (tiles * view.n_kv_heads > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
-    int64_t most_keys = std::min<int64_t>(d->table_width << view.page_shift, INT32_MAX - 255);
-    // a window bounds the keys of a tile: its own, those of its other tokens, and the step it begins in
-    if (d->window) most_keys = std::min<int64_t>(most_keys, d->window + 16 + 32);
-    const Choice c = choose(tiles * view.n_kv_heads, most_keys);
-    a->split_tokens = c.split_tokens;
-    a->n_split = c.n_split;
-    if (c.n_split > 1) {
-        const size_t rows = size_t(c.n_split) * a->n_tok * d->n_q_heads;
-        *ws_bytes = up256(rows * d->cache->head_dim * 4) + up256(rows * 8);
+    a->tiles_per = 0;
+    a->split_tokens = 0;
+    a->n_split = 1;
+    if (d->n_seq == 1 && d->cu_q) {  // it can only be the one request
+        a->cu_q = nullptr;
+        a->uniform_q = a->n_tok;
     }
+    const uint64_t heads = view.n_kv_heads, group = a->group;
+    const uint64_t bound = !a->cu_q ? a->uniform_q
+                                    : (d->max_q_len ? std::min<uint64_t>(d->max_q_len, a->n_tok) : a->n_tok);
+    const uint64_t most_rows = bound * group;
+    const int64_t all_keys = std::min<int64_t>(d->table_width << view.page_shift, INT32_MAX - 255);
+    out->many = *a;
+    out->any_few = a->cu_q || most_rows <= kFewRows;
+    out->any_many = most_rows > kFewRows;
+    out->few_o = out->few_ml = out->many_o = out->many_ml = 0;
+    // a window bounds the keys of a tile: its own, those of its other tokens, and the step it begins in
+    const auto keys_of = [&](uint64_t rows, int64_t step) {
+        return d->window ? std::min<int64_t>(all_keys, d->window + int64_t((rows + group - 1) / group) + step) : all_keys;
+    };
+    if (out->any_few) {
+        AttentionArgs& f = out->few;
+        f.max_rows = static_cast<uint32_t>(std::min<uint64_t>(most_rows, kFewRows));
+        f.tiles_per = (f.max_rows + kRowsTile - 1) / kRowsTile;
+        // without a bound the tiles as the lengths need them may be fewer
+        if (f.cu_q && uint64_t(f.n_tok) * group / kRowsTile + f.n_seq < uint64_t(f.tiles_per) * f.n_seq) f.tiles_per = 0;
+        const uint64_t groups = tile_count<kRowsTile>(f) * heads;
+        if (groups > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
+        const Split s = split_rows(groups, keys_of(std::min<uint64_t>(kRowsTile, f.max_rows), kRowsAlign));
+        f.split_tokens = s.tokens;
+        f.n_split = s.n;
+        if (s.n > 1) {
+            const size_t rows = size_t(s.n) * f.n_seq * heads * f.max_rows;
+            out->few_o = up256(rows * d->cache->head_dim * 4);
+            out->few_ml = up256(rows * 8);
+        }
+    }
+    if (out->any_many) {
+        AttentionArgs& m = out->many;
+        m.min_rows = out->any_few ? kFewRows + 1 : 0;
+        if (!m.cu_q) m.tiles_per = static_cast<uint32_t>((most_rows + kTileRows - 1) / kTileRows);
+        const uint64_t groups = tile_count<kTileRows>(m) * heads;
+        if (groups > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
+        const uint64_t all_rows = uint64_t(m.n_tok) * d->n_q_heads;
+        const Split s = split_tiles(groups, keys_of(kTileRows, kTileAlign), all_rows, d->cache->head_dim);
+        m.split_tokens = s.tokens;
+        m.n_split = s.n;
+        if (s.n > 1) {
+            out->many_o = up256(s.n * all_rows * d->cache->head_dim * 4);
+            out->many_ml = up256(s.n * all_rows * 8);
+        }
+    }
+    *ws_bytes = out->few_o + out->few_ml + out->many_o + out->many_ml;
     return ENGRAM_OK;
 }
 
@@ -232,27 +301,40 @@ int engram_kv_append(const engram_append_desc* d, void* stream) {
 
 int engram_paged_attention_workspace(const engram_attention_desc* d, size_t* bytes) {
     if (!bytes) return ENGRAM_EINVAL;
-    AttentionArgs a;
+    Launches l;
     size_t need = 0;
-    const int st = attention_args(d, &a, &need);
+    const int st = attention_args(d, &l, &need);
     if (st == ENGRAM_OK) *bytes = need;
     return st;
 }
 
 int engram_paged_attention(const engram_attention_desc* d, void* ws, size_t ws_bytes, void* stream) {
-    AttentionArgs a;
+    Launches l;
     size_t need = 0;
-    const int st = attention_args(d, &a, &need);
+    const int st = attention_args(d, &l, &need);
     if (st != ENGRAM_OK) return st;
     if (d->n_tok == 0) return ENGRAM_OK;
     if (need) {
         if (!ws || ws_bytes < need || !aligned(ws, 256)) return ENGRAM_EWORKSPACE;
-        const size_t rows = size_t(a.n_split) * a.n_tok * d->n_q_heads;
-        a.part_o = static_cast<float*>(ws);
-        a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + up256(rows * d->cache->head_dim * 4));
+        uint8_t* at = static_cast<uint8_t*>(ws);
+        l.few.part_o = reinterpret_cast<float*>(at);
+        l.few.part_ml = reinterpret_cast<float*>(at + l.few_o);
+        at += l.few_o + l.few_ml;
+        l.many.part_o = reinterpret_cast<float*>(at);
+        l.many.part_ml = reinterpret_cast<float*>(at + l.many_o);
     }
-    const hipError_t e = launch_paged_rows(a, d->cache->head_dim, d->type, d->cache->type == ENGRAM_E4M3,
-                                           static_cast<hipStream_t>(stream));
+    const hipStream_t to = static_cast<hipStream_t>(stream);
+    const uint32_t dim = d->cache->head_dim;
+    const bool e4m3 = d->cache->type == ENGRAM_E4M3;
+    hipError_t e = hipSuccess;
+    if (l.any_many) {
+        e = launch_paged_tile(l.many, dim, d->type, e4m3, to);
+        if (e == hipSuccess && l.many.n_split > 1) e = launch_paged_join(l.many, dim, d->type, e4m3, true, to);
+    }
+    if (e == hipSuccess && l.any_few) {
+        e = launch_paged_rows(l.few, dim, d->type, e4m3, to);
+        if (e == hipSuccess && l.few.n_split > 1) e = launch_paged_join(l.few, dim, d->type, e4m3, false, to);
+    }
     return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
 }
 
