@@ -562,4 +562,4 @@ def probe_rows(plan: Plan, addr: torch.Tensor, out: torch.Tensor, stream=None) -
     return out
 
 
-from .serving import kv_append, paged_attention, qk_norm_rope  # noqa: E402  (the binding above comes first)
+from .serving import kv_append, paged_attention, paged_attention_workspace, qk_norm_rope  # noqa: E402  (the binding above comes first)

@@ -1,4 +1,5 @@
-"""Build libengram.so (HIP kernels + C ABI) and libengram_measure.so (synthetic fill, probes) for gfx950 with hipcc.
+"""Build libengram.so (HIP kernels + C ABI) and libengram_measure.so (synthetic fill, probes) for gfx950 with hipcc, and
+_serving.so (the Python binding of the serving calls) with g++ against torch's headers.
 
 Usage: python hashed_gram_memory_amd/build.py   (run by path: importing the package needs the library)
 Cross-compiles without a GPU.  Object files go to _build/ next to this file.
@@ -24,6 +25,7 @@ SOURCES = ["engram_api.cpp", "hash.hip", "gather_reduce.hip", "dedup.hip", "look
            "gather_batched.hip", "dedup_noalloc.hip", "check.hip", "serving_api.cpp", "norm_rope.hip", "paged_rows.hip",
            "paged_tile.hip", "paged_join.hip"]
 MEASURE_SOURCES = ["synth_fill.hip", "probe.hip"]
+SERVING_BINDING = os.path.join(HERE, "_serving.so")
 MEASURE_LIB = os.path.join(HERE, "libengram_measure.so")
 ARCH = "gfx950"
 
@@ -52,6 +54,36 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """Host code only: no device pass, and no HIP header beyond what torch's own headers need."""
+    import sysconfig
+
+    import torch
+
+    top = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "serving_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-result", "-DUSE_ROCM",
+           "-D__HIP_PLATFORM_AMD__=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", os.path.join(top, "include"), "-isystem", os.path.join(top, "include/torch/csrc/api/include"),
+           "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "serving_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for serving_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    tmp = SERVING_BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-lengram", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _serving.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, SERVING_BINDING)
+
+
 def _link(objs, out) -> None:
     tmp = out + ".tmp%d" % os.getpid()
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -64,10 +96,12 @@ def _link(objs, out) -> None:
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = SOURCES + MEASURE_SOURCES
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = dict(zip(srcs, ex.map(_compile, srcs)))
     _link([objs[f] for f in SOURCES], LIB)
     _link([objs[f] for f in MEASURE_SOURCES], MEASURE_LIB)
+    _link_binding(binding.result())
     # A plain C consumer of the ABI (host code only), linked against the libraries just built.
     cmd = ["gcc", "-O2", "-std=c11", "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE, "-I", "/opt/rocm/include", DEMO_SRC,
            "-o", DEMO + ".tmp", "-L", HERE, "-lengram", "-lengram_measure", "-L", "/opt/rocm/lib", "-lamdhip64",
@@ -77,7 +111,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"c_abi_demo build failed:\n{r.stdout}\n{r.stderr}")
     os.replace(DEMO + ".tmp", DEMO)
     if verbose:
-        print("built", LIB, MEASURE_LIB, "and", DEMO)
+        print("built", LIB, MEASURE_LIB, SERVING_BINDING, "and", DEMO)
     return LIB
 
 
