@@ -20,8 +20,12 @@ struct AttentionArgs {
     const int32_t* kv_len;   // [n_seq]
     const int32_t* cu_q;     // [n_seq + 1], or nullptr: n_tok / n_seq tokens each
     CacheView cache;
-    float* part_o;           // [n_split][rows][dim] sums of a split, not divided (rows: part_index)
-    float* part_ml;          // [n_split][rows][2] maximum (in units of log2) and sum
+    // Parts of divided rows, not yet divided by their sums: sums of values, and (reference r, sum of weights) in
+    // units of 2^(x - r).  paged_tile.hip: [n_split][n_tok][n_q_heads][dim or 2]; paged_rows.hip: [n_work][2]
+    // [min(max_rows, 16)][dim or 2], and what there is to join.
+    float* part_o;
+    float* part_ml;
+    int4* part_job;          // [n_work]
     int64_t q_tok, q_head, out_tok, out_head;  // strides, elements
     int64_t table_stride;
     uint32_t table_width;
@@ -30,8 +34,9 @@ struct AttentionArgs {
     uint32_t uniform_q;      // tokens of each request where cu_q is nullptr
     uint32_t group;          // query heads per KV head
     uint32_t window;
-    uint32_t split_tokens;   // keys of a split; 0: one split takes all
+    uint32_t split_tokens;   // paged_tile.hip: keys of a split; 0: one split takes all
     uint32_t n_split;
+    uint32_t n_work;         // paged_rows.hip: workgroups that share the keys evenly; 0: a workgroup takes a tile
     uint32_t min_rows, max_rows;  // requests of this launch: min_rows <= rows <= max_rows
     uint32_t tiles_per;      // tiles set aside for each request; 0: as the lengths need (find_tile)
     float scale_log2;        // scale * log2(e)
@@ -126,24 +131,14 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& A, const Request& r
     return s;
 }
 
-// Where a divided row's parts lie.  Requests of few rows (max_rows) have that
-// many places each, so that their splits, which are many, need no room for the
-// rows of the long requests of the same call; the others lie by token and head.
-__device__ __forceinline__ uint64_t part_index(const AttentionArgs& A, uint32_t split, uint32_t b, uint32_t h,
-                                               uint32_t row, uint64_t flat) {
-    const uint64_t heads = A.cache.n_kv_heads;
-    if (A.max_rows != UINT32_MAX) return ((static_cast<uint64_t>(split) * A.n_seq + b) * heads + h) * A.max_rows + row;
-    return static_cast<uint64_t>(split) * A.n_tok * (heads * A.group) + flat;
-}
-
 constexpr uint32_t kRowsTile = 16;   // rows of a tile in paged_rows.hip
 constexpr uint32_t kTileRows = 256;  // and in paged_tile.hip
-// A split's keys begin at a multiple of this many: the keys of a step.
-constexpr int32_t kRowsAlign = 32, kTileAlign = 64;
+constexpr int32_t kRowsBlock = 128;  // keys that a workgroup of paged_rows.hip takes at a time
+constexpr int32_t kTileAlign = 64;   // a split's keys begin at a multiple of this many in paged_tile.hip
 
 hipError_t launch_paged_rows(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
 hipError_t launch_paged_tile(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
-// Joins the parts that a launch of either wrote (many: paged_tile.hip's).
-hipError_t launch_paged_join(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, bool many, hipStream_t stream);
+// Joins the parts of a divided launch of launch_paged_tile (launch_paged_rows joins its own).
+hipError_t launch_paged_join(const AttentionArgs& a, uint32_t dim, uint32_t type, hipStream_t stream);
 
 }  // namespace engram

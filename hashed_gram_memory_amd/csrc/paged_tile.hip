@@ -32,8 +32,9 @@
 // What a row does not see: scores of hidden keys become -inf before the
 // maximum; keys that no row sees (past the end, before the window, on a page
 // outside the pool) have zeros for V.  Where a tile that only some rows see
-// in full holds an infinity or NaN in V, its second product is done key by
-// key, so that no row meets a value that its mask hides.
+// in full holds infinities or NaN in V, they are replaced by zeros too, and
+// counted for the rows that see them by two more products, of ones (not below
+// +inf, not above -inf), so that no row meets a value that its mask hides.
 #include <type_traits>
 
 #include "paged_attention.h"
@@ -43,26 +44,6 @@ namespace {
 
 typedef short s16x4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4v lds_s16x4v;
-
-// p of a score at its row's reference; a term may pass the reference by 2^kSlack before the sums are rescaled.  fp16
-// holds p up to 2^14 and normal numbers down to 2^-14: 2^-21 of the reference.
-template <class P>
-struct Room;
-template <>
-struct Room<Bf16> {
-    static constexpr float kShift = 0.0f, kSlack = 8.0f;
-};
-template <>
-struct Room<F16> {
-    static constexpr float kShift = 7.0f, kSlack = 7.0f;
-};
-
-// the larger of a lane's value and that of the lane 32 away
-__device__ __forceinline__ float max_halves(float x) {
-    const uint32_t w = __builtin_bit_cast(uint32_t, x);
-    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-    return fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
-}
 
 // Block (16 bytes of 16-bit channels) of a key's LDS row where channel block c lies.
 template <int D>
@@ -95,7 +76,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     using P = std::conditional_t<kE4m3, Bf16, T>;   // P and V's type; e4m3 codes are exact in both types
     using Raw = std::conditional_t<kE4m3, u32x2v, u32x4v>;
     constexpr uint32_t ES = kE4m3 ? 1 : 2;
-    constexpr float kSlack = Room<P>::kSlack, kShift = Room<P>::kShift;
+    constexpr float kSlack = P::kSlack, kShift = P::kShift;
 
     __shared__ __attribute__((aligned(1024))) uint16_t sm_k[2][KT * D];
     __shared__ __attribute__((aligned(1024))) uint16_t sm_v[2][KT * D];
@@ -231,8 +212,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
             if ((absent >> i) & 1u) vw = u32x4v{0u, 0u, 0u, 0u};
             if (cut) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    odd |= (vw[j] & P::kExponent) == P::kExponent || ((vw[j] >> 16) & P::kExponent) == P::kExponent;
+                for (int j = 0; j < 4; ++j) odd |= P::nonfinite(vw[j]) != 0;
             }
             *reinterpret_cast<u32x4v*>(&sm_k[t & 1][r * D + k_block<D>(r, cb) * 8u]) = kw;
             *reinterpret_cast<u32x4v*>(&sm_v[t & 1][r * D + v_block<D>(r, cb) * 8u]) = vw;
@@ -309,7 +289,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
             for (int b = 0; b < TB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-            top = max_halves(top) * c;
+            top = max32(top) * c;
             if (__any(top > m + kSlack)) {
                 const float m_new = fmaxf(m, top);
                 const float nb_new = m_new == -INFINITY ? 0.0f : kShift - m_new;
@@ -352,50 +332,58 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
             }
 
             const uint16_t* vb = sm_v[t & 1];
-            if (whole || sm_odd[t & 3] == 0u) {
-                const uint32_t z = lane & 15u;  // of 16 lanes that read 4 keys of 16 channels
-                const uint32_t vrow = 4u * g + (z >> 2);
-                const uint32_t vcol = 2u * ((lane >> 4) & 1u) + ((z & 3u) >> 1);
-#pragma unroll
+            const uint32_t z = lane & 15u;  // of 16 lanes that read 4 keys of 16 channels
+            const uint32_t vrow = 4u * g + (z >> 2);
+            const uint32_t vcol = 2u * ((lane >> 4) & 1u) + ((z & 3u) >> 1);
+            // V's channels 32 f + n at the keys 16 st + 4g + 0..3 and 8 more; v_block takes the key's bits 0 and 1 only
+            auto values = [&](int st, int f) {
+                const uint32_t at = (16 * st + vrow) * D + v_block<D>(vrow, 4 * f + vcol) * 8u + 4u * (z & 1u);
+                const s16x4v x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at]);
+                const s16x4v x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at + 8 * D]);
+                const u32x2v w0 = __builtin_bit_cast(u32x2v, x0), w1 = __builtin_bit_cast(u32x2v, x1);
+                return u32x4v{w0[0], w0[1], w1[0], w1[1]};
+            };
+            const bool clean = whole || sm_odd[t & 3] == 0u;
+            if (!clean) {
+                // The rows that see infinities or NaN get them by counting; below, their places hold zeros.
+#pragma unroll 1
                 for (int st = 0; st < KT / 16; ++st) {
-                    u32x4v pw;
+                    const uint32_t bits = static_cast<uint32_t>(seen >> (16 * st + 4u * g));  // keys 0..3 and 8..11 of these
+                    u32x4v one;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) pw[j] = P::pack(s[st / 2][8 * (st % 2) + 2 * j], s[st / 2][8 * (st % 2) + 2 * j + 1]);
+                    for (int w = 0; w < 4; ++w) one[w] = P::ones((bits >> (8 * (w / 2) + 2 * (w % 2))) & 3u);
 #pragma unroll
                     for (int f = 0; f < FB; ++f) {
-                        // keys 16 st + 4g + 0..3 and 8 more; v_block takes the key's bits 0 and 1 only (D = 64: bit 1)
-                        const uint32_t at = (16 * st + vrow) * D + v_block<D>(vrow, 4 * f + vcol) * 8u + 4u * (z & 1u);
-                        const s16x4v x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at]);
-                        const s16x4v x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at + 8 * D]);
-                        const u32x2v w0 = __builtin_bit_cast(u32x2v, x0), w1 = __builtin_bit_cast(u32x2v, x1);
-                        o[f] = P::mfma32(u32x4v{w0[0], w0[1], w1[0], w1[1]}, pw, o[f]);
+                        const u32x4v a = values(st, f);
+                        u32x4v up, down;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            up[w] = P::not_below(a[w]);
+                            down[w] = P::not_above(a[w]);
+                        }
+                        f32x16v zero;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
+                        const f32x16v n_up = P::mfma32(up, one, zero), n_down = P::mfma32(down, one, zero);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[f][i] += (n_up[i] > 0.0f ? INFINITY : 0.0f) + (n_down[i] > 0.0f ? -INFINITY : 0.0f);
                     }
                 }
-            } else {
-                // Key by key: lane (n, g) adds p * V[its channels] for the keys that row n sees.
-#pragma unroll 1
-                for (uint32_t k = 0; k < KT; ++k) {
-                    const uint32_t from = (k >> 2) & 1u, at = ((k & 31u) >> 3) * 4u + (k & 3u);
-                    float pk = 0.0f;
+            }
 #pragma unroll
-                    for (int b = 0; b < TB; ++b)
+            for (int st = 0; st < KT / 16; ++st) {
+                u32x4v pw;
 #pragma unroll
-                        for (uint32_t i = 0; i < 16; ++i) pk = k / 32u == static_cast<uint32_t>(b) && at == i ? s[b][i] : pk;
-                    pk = __shfl(pk, static_cast<int>(n + 32u * from));
-                    if ((seen >> k) & 1u) {
+                for (int j = 0; j < 4; ++j) pw[j] = P::pack(s[st / 2][8 * (st % 2) + 2 * j], s[st / 2][8 * (st % 2) + 2 * j + 1]);
 #pragma unroll
-                        for (int f = 0; f < FB; ++f)
+                for (int f = 0; f < FB; ++f) {
+                    u32x4v a = values(st, f);
+                    if (!clean) {
 #pragma unroll
-                            for (uint32_t y = 0; y < 4; ++y) {
-                                const uint32_t ch = 32 * f + 8 * y + 4 * g;
-                                const u32x2v w = *reinterpret_cast<const u32x2v*>(&vb[k * D + v_block<D>(k, ch / 8u) * 8u + ch % 8u]);
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    o[f][4 * y + 2 * e] = __builtin_fmaf(pk, P::lo(w[e]), o[f][4 * y + 2 * e]);
-                                    o[f][4 * y + 2 * e + 1] = __builtin_fmaf(pk, P::hi(w[e]), o[f][4 * y + 2 * e + 1]);
-                                }
-                            }
+                        for (int w = 0; w < 4; ++w) a[w] &= ~P::nonfinite(a[w]);
                     }
+                    o[f] = P::mfma32(a, pw, o[f]);
                 }
             }
         }
@@ -407,12 +395,12 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
         __syncthreads();
     }
 
-    l += __shfl_xor(l, 32);
+    l = sum32(l);
     if (!alive || wrow0 + n >= rows) return;
     const uint32_t q_heads = heads * A.group;
     const uint64_t flat = static_cast<uint64_t>(tok) * q_heads + head;
     if (divided) {
-        const uint64_t at = part_index(A, split, tile.b, h, row, flat);
+        const uint64_t at = static_cast<uint64_t>(split) * A.n_tok * q_heads + flat;
         float* dst = A.part_o + at * D + 4 * g;
 #pragma unroll
         for (int f = 0; f < FB; ++f)
@@ -420,7 +408,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
             for (int y = 0; y < 4; ++y)
                 *reinterpret_cast<f32x4v*>(dst + 32 * f + 8 * y) =
                     f32x4v{o[f][4 * y], o[f][4 * y + 1], o[f][4 * y + 2], o[f][4 * y + 3]};
-        if (g == 0) *reinterpret_cast<f32x2v*>(A.part_ml + at * 2) = f32x2v{m == -INFINITY ? m : P::kShift - nb, l};
+        if (g == 0) *reinterpret_cast<f32x2v*>(A.part_ml + at * 2) = f32x2v{m == -INFINITY ? m : -nb, l};
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;

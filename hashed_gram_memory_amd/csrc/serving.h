@@ -19,8 +19,31 @@ typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2v __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8v __attribute__((ext_vector_type(8)));
 
-// The two 16-bit element types.  A register pair of them is one uint32_t.
-struct Bf16 {
+// What the two 16-bit element types share, by the bits of an exponent of all
+// ones and those of the number 1.  A register pair of them is one uint32_t.
+template <uint32_t kExp, uint32_t kUnit>
+struct Halves {
+    // all bits of each half that is an infinity or NaN: its exponent plus one carries into the sign's place
+    static __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
+        const uint32_t carry = ((w & (kExp * 0x10001u)) + kLow * 0x10001u) & 0x80008000u;
+        return (carry >> 15) * 0xFFFFu;
+    }
+    // the number 1 in each half that is +infinity or NaN (-infinity or NaN), 0 in the others
+    static __device__ __forceinline__ uint32_t not_below(uint32_t w) { return not_one(w, 0x8000u | kExp); }
+    static __device__ __forceinline__ uint32_t not_above(uint32_t w) { return not_one(w, kExp); }
+    // the number 1 or 0 in each half, by bits 0 and 1
+    static __device__ __forceinline__ uint32_t ones(uint32_t bits) { return ((bits & 1u) | (bits & 2u) << 15) * kUnit; }
+
+private:
+    static constexpr uint32_t kLow = kExp & (~kExp + 1u);  // the exponent's last place
+    static __device__ __forceinline__ uint32_t not_one(uint32_t w, uint32_t out) {
+        const uint32_t x = w ^ (out * 0x10001u);  // 0 in the halves that do not count
+        const uint32_t some = ((x & 0x7FFF7FFFu) + 0x7FFF7FFFu) | x;  // a half's sign: it is not 0
+        return ((nonfinite(w) & some & 0x80008000u) >> 15) * kUnit;
+    }
+};
+
+struct Bf16 : Halves<0x7F80u, 0x3F80u> {
     static __device__ __forceinline__ float lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
     static __device__ __forceinline__ float hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
     // round to nearest even
@@ -41,11 +64,12 @@ struct Bf16 {
     static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, kHigh));
     }
-    static constexpr uint32_t kExponent = 0x7F80u;  // all ones: infinity or NaN
-    static constexpr float kShift = 0.0f;
+    // Softmax terms are held as 2^kShift at their row's reference, and may pass
+    // it by 2^kSlack before the reference moves.
+    static constexpr float kShift = 0.0f, kSlack = 8.0f;
 };
 
-struct F16 {
+struct F16 : Halves<0x7C00u, 0x3C00u> {
     static __device__ __forceinline__ float lo(uint32_t w) {
         return static_cast<float>(__builtin_bit_cast(f16x2v, w)[0]);
     }
@@ -68,12 +92,38 @@ struct F16 {
     static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, kHigh));
     }
-    static constexpr uint32_t kExponent = 0x7C00u;
-    // Softmax terms are held times 2^14 (at most 16,384): 1 is fp16's 2^14, so
-    // a term of 2^-28 is still a normal number, where fp16 alone would lose the
-    // digits below 2^-14 and the terms below 2^-25.
-    static constexpr float kShift = 14.0f;
+    // fp16 ends at 65,504 and has all its digits down to 2^-14: with a term of
+    // 2^14 at most, one of 2^-21 of the reference is still a normal number.
+    static constexpr float kShift = 7.0f, kSlack = 7.0f;
 };
+
+// The larger, and the sum, of a lane's value and that of the lane 16 (32) away.
+__device__ __forceinline__ f32x2v swap16(float x) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return f32x2v{__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1]))};
+}
+__device__ __forceinline__ f32x2v swap32(float x) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return f32x2v{__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1]))};
+}
+__device__ __forceinline__ float max16(float x) {
+    const f32x2v r = swap16(x);
+    return fmaxf(r[0], r[1]);
+}
+__device__ __forceinline__ float max32(float x) {
+    const f32x2v r = swap32(x);
+    return fmaxf(r[0], r[1]);
+}
+__device__ __forceinline__ float sum16(float x) {
+    const f32x2v r = swap16(x);
+    return r[0] + r[1];
+}
+__device__ __forceinline__ float sum32(float x) {
+    const f32x2v r = swap32(x);
+    return r[0] + r[1];
+}
 
 // The paged cache as the kernels see it: K and V each [n_pages][n_kv_heads]
 // [page][dim], page p starting at p * page_stride elements; an e4m3 cache

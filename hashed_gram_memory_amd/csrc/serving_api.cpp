@@ -62,20 +62,6 @@ struct Split {
     uint32_t tokens, n;  // keys of a split (0: all), splits
 };
 
-// Few rows (paged_rows.hip).  A workgroup takes 128 keys at a time, and the
-// chip needs several workgroups on each of its 256 CUs; the keys of a tile are
-// halved until there are that many, or a split is 256 keys long.
-Split split_rows(uint64_t groups, int64_t most_keys) {
-    constexpr uint64_t kEnough = 2048;
-    constexpr int64_t kLeast = 256;
-    int64_t split = kLeast;
-    while (split < most_keys && groups * static_cast<uint64_t>((most_keys + 2 * split - 1) / (2 * split)) >= kEnough)
-        split *= 2;
-    while ((most_keys + split - 1) / split > 1024) split *= 2;
-    const uint32_t n = static_cast<uint32_t>(std::max<int64_t>(1, (most_keys + split - 1) / split));
-    return {n > 1 ? static_cast<uint32_t>(split) : 0u, n};
-}
-
 // Many rows (paged_tile.hip).  A workgroup fills a CU, so a launch takes
 // ceil(groups * n / 256) rounds of a split's keys, and joining writes and reads
 // n fp32 rows for each row; of up to 32 splits the one with the least of both.
@@ -98,14 +84,17 @@ Split split_tiles(uint64_t groups, int64_t most_keys, uint64_t rows, uint32_t di
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Rows of a request and KV head up to which paged_rows.hip takes it.
-constexpr uint32_t kFewRows = 64;
+// Rows of a request and KV head up to which paged_rows.hip takes it, which
+// reads the keys once for every 16 rows: 8 requests over 8,192 keys (8 KV heads,
+// head_dim 128, bf16) take 59 us there with 32 rows each and 131 with 40, and 94
+// in paged_tile.hip with 64.
+constexpr uint32_t kFewRows = 32;
 
 // A call's launches: the requests of few rows, those of many, or both.
 struct Launches {
     AttentionArgs few, many;
     bool any_few, any_many;
-    size_t few_o, few_ml, many_o, many_ml;  // bytes of their parts
+    size_t few_o, few_ml, few_job, many_o, many_ml;  // bytes of their parts
 };
 
 // Checks a description and fills the kernels' arguments (without the workspace).
@@ -163,6 +152,8 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     a->tiles_per = 0;
     a->split_tokens = 0;
     a->n_split = 1;
+    a->n_work = 0;
+    a->part_job = nullptr;
     if (d->n_seq == 1 && d->cu_q) {  // it can only be the one request
         a->cu_q = nullptr;
         a->uniform_q = a->n_tok;
@@ -175,7 +166,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     out->many = *a;
     out->any_few = a->cu_q || most_rows <= kFewRows;
     out->any_many = most_rows > kFewRows;
-    out->few_o = out->few_ml = out->many_o = out->many_ml = 0;
+    out->few_o = out->few_ml = out->few_job = out->many_o = out->many_ml = 0;
     // a window bounds the keys of a tile: its own, those of its other tokens, and the step it begins in
     const auto keys_of = [&](uint64_t rows, int64_t step) {
         return d->window ? std::min<int64_t>(all_keys, d->window + int64_t((rows + group - 1) / group) + step) : all_keys;
@@ -188,13 +179,20 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         if (f.cu_q && uint64_t(f.n_tok) * group / kRowsTile + f.n_seq < uint64_t(f.tiles_per) * f.n_seq) f.tiles_per = 0;
         const uint64_t groups = tile_count<kRowsTile>(f) * heads;
         if (groups > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
-        const Split s = split_rows(groups, keys_of(std::min<uint64_t>(kRowsTile, f.max_rows), kRowsAlign));
-        f.split_tokens = s.tokens;
-        f.n_split = s.n;
-        if (s.n > 1) {
-            const size_t rows = size_t(s.n) * f.n_seq * heads * f.max_rows;
+        // Few keys: a workgroup takes a tile by itself, without the second launch that joins the parts (bf16, 8 KV heads,
+        // head_dim 128: one request of 512 keys 8.2 us against 9.4 divided, of 1,024 12.5 against 9.5; where there are
+        // tiles for every CU, 64 requests of 1,024 keys 40.8 against 43.5).  Else 512 workgroups share all keys: two on
+        // each CU keep HBM as busy as three or four do (64 requests of up to 8,192 keys 216 us against 224 and 224), and
+        // leave fewer parts to join.
+        const int64_t keys = keys_of(f.max_rows, 32);
+        const int64_t blocks = (keys + kRowsBlock - 1) / kRowsBlock;
+        const bool whole = blocks * d->cache->head_dim <= 512 || (groups >= 512 && blocks <= 8) || groups * blocks >> 31;
+        f.n_work = whole ? 0u : static_cast<uint32_t>(std::min<uint64_t>(groups * blocks, 512));
+        if (f.n_work) {
+            const size_t rows = size_t(f.n_work) * 2 * std::min(f.max_rows, kRowsTile);
             out->few_o = up256(rows * d->cache->head_dim * 4);
             out->few_ml = up256(rows * 8);
+            out->few_job = up256(f.n_work * sizeof(int4));
         }
     }
     if (out->any_many) {
@@ -212,7 +210,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
             out->many_ml = up256(s.n * all_rows * 8);
         }
     }
-    *ws_bytes = out->few_o + out->few_ml + out->many_o + out->many_ml;
+    *ws_bytes = out->few_o + out->few_ml + out->few_job + out->many_o + out->many_ml;
     return ENGRAM_OK;
 }
 
@@ -319,7 +317,8 @@ int engram_paged_attention(const engram_attention_desc* d, void* ws, size_t ws_b
         uint8_t* at = static_cast<uint8_t*>(ws);
         l.few.part_o = reinterpret_cast<float*>(at);
         l.few.part_ml = reinterpret_cast<float*>(at + l.few_o);
-        at += l.few_o + l.few_ml;
+        l.few.part_job = reinterpret_cast<int4*>(at + l.few_o + l.few_ml);
+        at += l.few_o + l.few_ml + l.few_job;
         l.many.part_o = reinterpret_cast<float*>(at);
         l.many.part_ml = reinterpret_cast<float*>(at + l.many_o);
     }
@@ -329,12 +328,9 @@ int engram_paged_attention(const engram_attention_desc* d, void* ws, size_t ws_b
     hipError_t e = hipSuccess;
     if (l.any_many) {
         e = launch_paged_tile(l.many, dim, d->type, e4m3, to);
-        if (e == hipSuccess && l.many.n_split > 1) e = launch_paged_join(l.many, dim, d->type, e4m3, true, to);
+        if (e == hipSuccess && l.many.n_split > 1) e = launch_paged_join(l.many, dim, d->type, to);
     }
-    if (e == hipSuccess && l.any_few) {
-        e = launch_paged_rows(l.few, dim, d->type, e4m3, to);
-        if (e == hipSuccess && l.few.n_split > 1) e = launch_paged_join(l.few, dim, d->type, e4m3, false, to);
-    }
+    if (e == hipSuccess && l.any_few) e = launch_paged_rows(l.few, dim, d->type, e4m3, to);
     return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
 }
 
