@@ -78,12 +78,11 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     constexpr uint32_t ES = kE4m3 ? 1 : 2;
     constexpr float kSlack = P::kSlack, kShift = P::kShift;
 
-    __shared__ __attribute__((aligned(1024))) uint16_t sm_k[2][KT * D];
-    __shared__ __attribute__((aligned(1024))) uint16_t sm_v[2][KT * D];
-    __shared__ __attribute__((aligned(16))) float sm_scale[2][2][kE4m3 ? KT : 4];
-    __shared__ int32_t sm_page[2][KT];       // page of each key, -1: absent
-    __shared__ uint64_t sm_there[4];         // keys that are there, by bit
-    __shared__ uint32_t sm_odd[4];           // not 0: V holds an infinity or NaN (only looked for where a mask cuts the tile)
+    __shared__ __attribute__((aligned(1024))) uint16_t sm_k[3][KT * D];
+    __shared__ __attribute__((aligned(1024))) uint16_t sm_v[4][KT * D];
+    __shared__ __attribute__((aligned(16))) float sm_scale[4][2][kE4m3 ? KT : 4];
+    __shared__ int32_t sm_page[4][KT];       // page of each key, -1: absent
+    __shared__ uint64_t sm_there[8];         // keys that are there, by bit
 
     const uint32_t heads = A.cache.n_kv_heads;
     const uint32_t tile_at = blockIdx.x / heads, h = blockIdx.x - tile_at * heads;
@@ -150,203 +149,275 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
 
     const uint32_t shift = A.cache.page_shift, in_page = (1u << shift) - 1u;
     const int32_t* table = A.table + tile.b * A.table_stride;
+    const uint8_t* const kh = A.cache.k + (static_cast<int64_t>(h) << shift) * D * ES;
+    const uint8_t* const vh = A.cache.v + (static_cast<int64_t>(h) << shift) * D * ES;
 
-    // page of key `base + lane` (wave 0), -1 where no row sees it or there is no such page
-    auto ask_page = [&](int32_t base) -> int32_t {
-        const int32_t key = base + static_cast<int32_t>(lane);
+    const auto base_of = [&](int32_t t) { return c0 + t * KT; };
+    // page of the tile's key `lane` (wave 0), -1 where no row sees it or there is no such page
+    const auto ask_page = [&](int32_t t) -> int32_t {
+        const int64_t key = static_cast<int64_t>(c0) + static_cast<int64_t>(t) * KT + lane;
         if (key >= c1 || key < span.lo || lane >= KT) return -1;
         const int32_t p = table[static_cast<uint32_t>(key) >> shift];
         return p >= 0 && p < A.cache.n_pages ? p : -1;
     };
-    auto tell_page = [&](int32_t t, int32_t page) {
-        if (lane < KT) sm_page[t & 1][lane] = page;
+    const auto tell_page = [&](int32_t t, int32_t page) {
+        if (lane < KT) sm_page[t & 3][lane] = page;
         const uint64_t there = __ballot(page >= 0);
-        if (lane == 0) {
-            sm_there[t & 3] = there;
-            sm_odd[t & 3] = 0;
-        }
+        if (lane == 0) sm_there[t & 7] = there;
     };
 
-    Raw kraw[NL], vraw[NL];
-    float sraw = 0.0f;
-    uint32_t absent = 0;  // bit i: block i belongs to an absent key
-    auto ask = [&](int32_t t) {
-        const int32_t base = c0 + t * KT;
-        absent = 0;
+    struct Blocks {
+        Raw k[NL], v[NL];
+        float scale;
+        uint32_t absent;  // bit i: block i belongs to an absent key
+    };
+    const auto ask = [&](int32_t t) {
+        Blocks r;
+        r.absent = 0;
+        r.scale = 0.0f;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const uint32_t at = i * kThreads + tid, r = at / CB, cb = at % CB;
-            const int32_t page = sm_page[t & 1][r];
-            if (page < 0) absent |= 1u << i;
-            const int64_t in = (static_cast<int64_t>(h) << shift) + ((base + static_cast<int32_t>(r)) & in_page);
+            const uint32_t at = i * kThreads + tid, row_at = at / CB, cb = at % CB;
+            const int32_t page = sm_page[t & 3][row_at];
+            if (page < 0) r.absent |= 1u << i;
+            const uint32_t in = ((static_cast<uint32_t>(base_of(t)) + row_at) & in_page) * D + cb * 8u;
             const int64_t p0 = max(page, 0);
-            kraw[i] = *reinterpret_cast<const Raw*>(A.cache.k + (p0 * A.cache.k_page_stride + in * D + cb * 8u) * ES);
-            vraw[i] = *reinterpret_cast<const Raw*>(A.cache.v + (p0 * A.cache.v_page_stride + in * D + cb * 8u) * ES);
+            r.k[i] = *reinterpret_cast<const Raw*>(kh + (p0 * A.cache.k_page_stride + in) * ES);
+            r.v[i] = *reinterpret_cast<const Raw*>(vh + (p0 * A.cache.v_page_stride + in) * ES);
         }
         if constexpr (kE4m3) {
             if (tid < 2u * KT) {
-                const uint32_t r = tid % KT;
-                const int32_t page = sm_page[t & 1][r];
-                const int64_t in = (static_cast<int64_t>(h) << shift) + ((base + static_cast<int32_t>(r)) & in_page);
-                const float* s = tid < KT ? A.cache.k_scale : A.cache.v_scale;
-                sraw = s[((static_cast<int64_t>(max(page, 0)) * heads) << shift) + in];
-                if (page < 0) sraw = 0.0f;
+                const uint32_t row_at = tid % KT;
+                const int32_t page = sm_page[t & 3][row_at];
+                const uint32_t in = (static_cast<uint32_t>(base_of(t)) + row_at) & in_page;
+                const float* from = tid < KT ? A.cache.k_scale : A.cache.v_scale;
+                r.scale = from[((static_cast<int64_t>(max(page, 0)) * heads + h) << shift) + in];
+                if (page < 0) r.scale = 0.0f;
             }
         }
+        return r;
     };
-    auto put = [&](int32_t t) {
-        const int32_t base = c0 + t * KT;
-        const bool cut = base < last_row.lo || base + KT > first_row.hi;
-        bool odd = false;
+    const auto put = [&](int32_t t, const Blocks& r) {
+        const uint32_t kt = static_cast<uint32_t>(t) % 3u;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const uint32_t at = i * kThreads + tid, r = at / CB, cb = at % CB;
+            const uint32_t at = i * kThreads + tid, row_at = at / CB, cb = at % CB;
             u32x4v kw, vw;
             if constexpr (kE4m3) {
-                kw = widen<T>(kraw[i]);
-                vw = widen<P>(vraw[i]);
+                kw = widen<T>(r.k[i]);
+                vw = widen<P>(r.v[i]);
             } else {
-                kw = kraw[i];
-                vw = vraw[i];
+                kw = r.k[i];
+                vw = r.v[i];
             }
-            if ((absent >> i) & 1u) vw = u32x4v{0u, 0u, 0u, 0u};
-            if (cut) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) odd |= P::nonfinite(vw[j]) != 0;
-            }
-            *reinterpret_cast<u32x4v*>(&sm_k[t & 1][r * D + k_block<D>(r, cb) * 8u]) = kw;
-            *reinterpret_cast<u32x4v*>(&sm_v[t & 1][r * D + v_block<D>(r, cb) * 8u]) = vw;
+            if ((r.absent >> i) & 1u) vw = u32x4v{0u, 0u, 0u, 0u};
+            *reinterpret_cast<u32x4v*>(&sm_k[kt][row_at * D + k_block<D>(row_at, cb) * 8u]) = kw;
+            *reinterpret_cast<u32x4v*>(&sm_v[t & 3][row_at * D + v_block<D>(row_at, cb) * 8u]) = vw;
         }
         if constexpr (kE4m3) {
-            if (tid < 2u * KT) sm_scale[t & 1][tid / KT][tid % KT] = sraw;
+            if (tid < 2u * KT) sm_scale[t & 3][tid / KT][tid % KT] = r.scale;
         }
-        if (odd) sm_odd[t & 3] = 1u;
     };
 
-    if (n_tiles > 0) {
-        if (wave == 0) {
-            const int32_t p0 = ask_page(c0), p1 = ask_page(c0 + KT);
-            tell_page(0, p0);
-            tell_page(1, p1);
-        }
-        __syncthreads();
-        ask(0);
-        put(0);
-        __syncthreads();
-    }
-
-    for (int32_t t = 0; t < n_tiles; ++t) {
-        const int32_t base = c0 + t * KT;
-        const bool more = t + 1 < n_tiles;
-        int32_t page2 = -1;
-        if (more) ask(t + 1);
-        if (wave == 0 && more) page2 = ask_page(base + 2 * KT);
-
-        // nothing to do for a wave without rows, or whose rows do not reach this tile
-        if (alive && base < wlast_row.hi && base + KT > wfirst_row.lo) {
-            const uint16_t* kb = sm_k[t & 1];
-            f32x16v s[TB];
+    f32x16v s[TB];       // scores, then softmax terms
+    u32x4v pw[KT / 16];  // P in 16 bits
+    // S^T = K Q^T
+    const auto scores = [&](int32_t t) {
+        const uint16_t* kb = sm_k[static_cast<uint32_t>(t) % 3u];
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                const u32x4v a = *reinterpret_cast<const u32x4v*>(&kb[(32 * b + n) * D + k_block<D>(n, 2 * i + g) * 8u]);
+                s[b] = T::mfma32(a, q[i], s[b]);
+            }
+    };
+    // V's channels 32 f + n at the keys 16 st + 4g + 0..3 and 8 more; v_block takes the key's bits 0 and 1 only
+    const auto values = [&](int32_t t, int st, int f) {
+        const uint16_t* vb = sm_v[t & 3];
+        const uint32_t z = lane & 15u;  // of 16 lanes that read 4 keys of 16 channels
+        const uint32_t vrow = 4u * g + (z >> 2), vcol = 2u * ((lane >> 4) & 1u) + ((z & 3u) >> 1);
+        const uint32_t at = (16 * st + vrow) * D + v_block<D>(vrow, 4 * f + vcol) * 8u + 4u * (z & 1u);
+        const s16x4v x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at]);
+        const s16x4v x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at + 8 * D]);
+        const u32x2v w0 = __builtin_bit_cast(u32x2v, x0), w1 = __builtin_bit_cast(u32x2v, x1);
+        return u32x4v{w0[0], w0[1], w1[0], w1[1]};
+    };
+    // O^T += V^T P^T
+    const auto sums = [&](int32_t t) {
+#pragma unroll
+        for (int st = 0; st < KT / 16; ++st)
+#pragma unroll
+            for (int f = 0; f < FB; ++f) o[f] = P::mfma32(values(t, st, f), pw[st], o[f]);
+    };
+    constexpr uint64_t kAll = KT == 64 ? ~uint64_t(0) : (uint64_t(1) << (KT & 63)) - 1u;
+    const auto seen_of = [&](int32_t t) {  // the tile's keys that this lane's row sees
+        const int32_t base = base_of(t);
+        const int32_t lo = min(max(see_lo - base, 0), KT), hi = min(max(pos + 1 - base, 0), KT);
+        const uint64_t below = lo >= 64 ? 0u : ~uint64_t(0) << lo, above = hi >= 64 ? 0u : ~uint64_t(0) << hi;
+        return sm_there[t & 7] & below & ~above;
+    };
+    // scores to P; the sums follow the reference
+    const auto softmax = [&](int32_t t) {
+        if constexpr (kE4m3) {
 #pragma unroll
             for (int b = 0; b < TB; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+                for (int y = 0; y < 4; ++y) {
+                    const f32x4v ks = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 3][0][32 * b + 8 * y + 4 * g]);
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-#pragma unroll
-                for (int b = 0; b < TB; ++b) {
-                    const u32x4v a = *reinterpret_cast<const u32x4v*>(&kb[(32 * b + n) * D + k_block<D>(n, 2 * i + g) * 8u]);
-                    s[b] = T::mfma32(a, q[i], s[b]);
+                    for (int z = 0; z < 4; ++z) s[b][4 * y + z] *= ks[z];
                 }
-            if constexpr (kE4m3) {
+        }
+        const int32_t base = base_of(t);
+        const bool whole = base >= wlast_row.lo && base + KT <= wfirst_row.hi && sm_there[t & 7] == kAll;
+        uint64_t seen = kAll;
+        if (!whole) {
+            seen = seen_of(t);
 #pragma unroll
-                for (int b = 0; b < TB; ++b)
+            for (int b = 0; b < TB; ++b) {
+                const uint32_t bits = static_cast<uint32_t>(seen >> (32 * b)) >> (4u * g);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const f32x4v ks = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 1][0][32 * b + 8 * y + 4 * g]);
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) s[b][4 * y + z] *= ks[z];
-                    }
+                for (int i = 0; i < 16; ++i) s[b][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[b][i] : -INFINITY;
             }
-
-            const uint64_t there = sm_there[t & 3];
-            constexpr uint64_t kAll = KT == 64 ? ~uint64_t(0) : (uint64_t(1) << (KT & 63)) - 1u;
-            const bool whole = base >= wlast_row.lo && base + KT <= wfirst_row.hi && there == kAll;
-            uint64_t seen = kAll;  // keys that this lane's row sees
-            if (!whole) {
-                const int32_t lo = min(max(see_lo - base, 0), KT), hi = min(max(pos + 1 - base, 0), KT);
-                const uint64_t below = lo >= 64 ? 0u : ~uint64_t(0) << lo, above = hi >= 64 ? 0u : ~uint64_t(0) << hi;
-                seen = there & below & ~above;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+        top = max32(top) * c;
+        if (__any(top > m + kSlack)) {
+            const float m_new = fmaxf(m, top);
+            const float nb_new = m_new == -INFINITY ? 0.0f : kShift - m_new;
+            const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(nb_new - nb);
+            l *= alpha;
+#pragma unroll
+            for (int f = 0; f < FB; ++f)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[f][i] *= alpha;
+            m = m_new;
+            nb = nb_new;
+        }
+        float part[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, nb));
+                part[i & 1] += s[b][i];
+            }
+        l += part[0] + part[1];
+        if constexpr (kE4m3) {
+#pragma unroll
+            for (int b = 0; b < TB; ++b)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const f32x4v vs = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 3][1][32 * b + 8 * y + 4 * g]);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) s[b][4 * y + z] *= vs[z];
+                }
+            if (!whole) {  // 0 * NaN
 #pragma unroll
                 for (int b = 0; b < TB; ++b) {
                     const uint32_t bits = static_cast<uint32_t>(seen >> (32 * b)) >> (4u * g);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[b][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[b][i] : -INFINITY;
+                    for (int i = 0; i < 16; ++i) s[b][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[b][i] : 0.0f;
                 }
             }
-            float top = -INFINITY;
+        }
 #pragma unroll
-            for (int b = 0; b < TB; ++b)
+        for (int st = 0; st < KT / 16; ++st)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-            top = max32(top) * c;
-            if (__any(top > m + kSlack)) {
-                const float m_new = fmaxf(m, top);
-                const float nb_new = m_new == -INFINITY ? 0.0f : kShift - m_new;
-                const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(nb_new - nb);
-                l *= alpha;
-#pragma unroll
-                for (int f = 0; f < FB; ++f)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[f][i] *= alpha;
-                m = m_new;
-                nb = nb_new;
-            }
-            float part[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int b = 0; b < TB; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, nb));
-                    part[i & 1] += s[b][i];
-                }
-            l += part[0] + part[1];
-            if constexpr (kE4m3) {
-#pragma unroll
-                for (int b = 0; b < TB; ++b)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const f32x4v vs = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 1][1][32 * b + 8 * y + 4 * g]);
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) s[b][4 * y + z] *= vs[z];
-                    }
-                if (!whole) {  // 0 * NaN
-#pragma unroll
-                    for (int b = 0; b < TB; ++b) {
-                        const uint32_t bits = static_cast<uint32_t>(seen >> (32 * b)) >> (4u * g);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            s[b][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[b][i] : 0.0f;
-                    }
-                }
-            }
+            for (int j = 0; j < 4; ++j) pw[st][j] = P::pack(s[st / 2][8 * (st % 2) + 2 * j], s[st / 2][8 * (st % 2) + 2 * j + 1]);
+    };
+    // the end of a phase: what it wrote to LDS is there, and nothing moves across
+    const auto phase = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        __builtin_amdgcn_sched_barrier(0);
+    };
 
-            const uint16_t* vb = sm_v[t & 1];
-            const uint32_t z = lane & 15u;  // of 16 lanes that read 4 keys of 16 channels
-            const uint32_t vrow = 4u * g + (z >> 2);
-            const uint32_t vcol = 2u * ((lane >> 4) & 1u) + ((z & 3u) >> 1);
-            // V's channels 32 f + n at the keys 16 st + 4g + 0..3 and 8 more; v_block takes the key's bits 0 and 1 only
-            auto values = [&](int st, int f) {
-                const uint32_t at = (16 * st + vrow) * D + v_block<D>(vrow, 4 * f + vcol) * 8u + 4u * (z & 1u);
-                const s16x4v x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at]);
-                const s16x4v x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at + 8 * D]);
-                const u32x2v w0 = __builtin_bit_cast(u32x2v, x0), w1 = __builtin_bit_cast(u32x2v, x1);
-                return u32x4v{w0[0], w0[1], w1[0], w1[1]};
-            };
-            const bool clean = whole || sm_odd[t & 3] == 0u;
-            if (!clean) {
-                // The rows that see infinities or NaN get them by counting; below, their places hold zeros.
+    // Two halves of the workgroup, a wave of each on every SIMD, take turns: while one does the products of its turn t
+    // (the scores of tile t + 1, the sums of tile t), the other does the softmax of its own and brings tiles.  A tile that is
+    // put in turn t is first read in turn t + 2, by when both halves have put their blocks.
+    if (n_tiles > 0) {
+        Blocks blocks;
+        int32_t page = -1;  // of a tile whose places are not yet free
+        if (wave == 0) {
+            const int32_t p0 = ask_page(0), p1 = ask_page(1), p2 = ask_page(2), p3 = ask_page(3);
+            page = ask_page(4);
+            tell_page(0, p0);
+            tell_page(1, p1);
+            tell_page(2, p2);
+            tell_page(3, p3);
+        }
+        phase();
+        {
+            const Blocks b0 = ask(0), b1 = ask(1);
+            blocks = ask(2);
+            put(0, b0);
+            put(1, b1);
+        }
+        phase();
+        const auto bring = [&](int32_t t) {  // tile t into LDS, the next into registers
+            if (t >= n_tiles) return;
+            put(t, blocks);
+            if (t + 1 < n_tiles) blocks = ask(t + 1);
+            if (wave == 0) {
+                tell_page(t + 2, page);
+                page = ask_page(t + 3);
+            }
+        };
+        if (wave >= kWaves / 2) phase();
+        scores(0);
+        phase();
+        softmax(0);
+        bring(2);
+        phase();
+        for (int32_t t = 0; t + 1 < n_tiles; ++t) {
+            scores(t + 1);
+            sums(t);
+            phase();
+            softmax(t + 1);
+            bring(t + 3);
+            phase();
+        }
+        sums(n_tiles - 1);
+        if (wave < kWaves / 2) phase();
+    }
+
+    // A NaN in the sums may be there by right, or come from 0 * infinity or 0 * NaN of a value that its row's mask hides:
+    // the keys again, tile by tile, with infinities and NaN counted for the rows that see them and zeros in their places.
+    bool nan = false;
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) nan |= o[f][i] != o[f][i];
+    if (__builtin_expect(__syncthreads_or(nan), 0)) {
+        m = -INFINITY;
+        nb = l = 0.0f;
+#pragma unroll
+        for (int f = 0; f < FB; ++f)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[f][i] = 0.0f;
 #pragma unroll 1
+        for (int32_t t = 0; t < n_tiles; ++t) {
+            if (wave == 0) tell_page(t, ask_page(t));
+            phase();
+            put(t, ask(t));
+            phase();
+            {
+                scores(t);
+                softmax(t);
+                const uint64_t seen = seen_of(t);
+#pragma unroll
                 for (int st = 0; st < KT / 16; ++st) {
                     const uint32_t bits = static_cast<uint32_t>(seen >> (16 * st + 4u * g));  // keys 0..3 and 8..11 of these
                     u32x4v one;
@@ -354,45 +425,31 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
                     for (int w = 0; w < 4; ++w) one[w] = P::ones((bits >> (8 * (w / 2) + 2 * (w % 2))) & 3u);
 #pragma unroll
                     for (int f = 0; f < FB; ++f) {
-                        const u32x4v a = values(st, f);
-                        u32x4v up, down;
+                        u32x4v a = values(t, st, f), up, down;
+                        f32x16v zero;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             up[w] = P::not_below(a[w]);
                             down[w] = P::not_above(a[w]);
+                            a[w] &= ~P::nonfinite(a[w]);
                         }
-                        f32x16v zero;
+                        const f32x16v n_up = P::mfma32(up, one, zero);
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
-                        const f32x16v n_up = P::mfma32(up, one, zero), n_down = P::mfma32(down, one, zero);
+                        for (int i = 0; i < 16; ++i) o[f][i] += n_up[i] > 0.0f ? INFINITY : 0.0f;
+                        const f32x16v n_down = P::mfma32(down, one, zero);
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[f][i] += (n_up[i] > 0.0f ? INFINITY : 0.0f) + (n_down[i] > 0.0f ? -INFINITY : 0.0f);
+                        for (int i = 0; i < 16; ++i) o[f][i] += n_down[i] > 0.0f ? -INFINITY : 0.0f;
+                        o[f] = P::mfma32(a, pw[st], o[f]);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
-#pragma unroll
-            for (int st = 0; st < KT / 16; ++st) {
-                u32x4v pw;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) pw[j] = P::pack(s[st / 2][8 * (st % 2) + 2 * j], s[st / 2][8 * (st % 2) + 2 * j + 1]);
-#pragma unroll
-                for (int f = 0; f < FB; ++f) {
-                    u32x4v a = values(st, f);
-                    if (!clean) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) a[w] &= ~P::nonfinite(a[w]);
-                    }
-                    o[f] = P::mfma32(a, pw, o[f]);
-                }
-            }
+            phase();
         }
-
-        if (more) {
-            put(t + 1);
-            if (wave == 0) tell_page(t + 2, page2);
-        }
-        __syncthreads();
     }
 
     l = sum32(l);
