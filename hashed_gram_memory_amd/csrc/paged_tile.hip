@@ -55,6 +55,26 @@ __device__ __forceinline__ uint32_t v_block(uint32_t key, uint32_t c) {
     return D == 64 ? c ^ (((key >> 1) & 1u) << 2) : c ^ ((key & 3u) << 2);
 }
 
+// The order of a turn's products: kScores of them with one LDS read each, kSums with two, the reads kAhead products
+// early, which is what LDS takes to answer.  (Left to itself, the compiler reads one product early.)
+template <int kScores, int kSums>
+__device__ __forceinline__ void products_in_order() {
+    constexpr int kMfma = 0x8, kRead = 0x100, kAhead = 6;
+    static_assert(kScores >= kAhead && kSums >= kAhead, "");
+    __builtin_amdgcn_sched_group_barrier(kRead, kAhead, 0);
+#pragma unroll
+    for (int i = 0; i < kScores - kAhead; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kMfma, kAhead, 0);
+}
+
 // eight e4m3 codes as 16-bit numbers
 template <class T>
 __device__ __forceinline__ u32x4v widen(u32x2v w) {
@@ -81,7 +101,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     __shared__ __attribute__((aligned(1024))) uint16_t sm_k[3][KT * D];
     __shared__ __attribute__((aligned(1024))) uint16_t sm_v[4][KT * D];
     __shared__ __attribute__((aligned(16))) float sm_scale[4][2][kE4m3 ? KT : 4];
-    __shared__ int32_t sm_page[4][KT];       // page of each key, -1: absent
+    __shared__ int32_t sm_page[8][KT];       // page of each key, -1: absent
     __shared__ uint64_t sm_there[8];         // keys that are there, by bit
 
     const uint32_t heads = A.cache.n_kv_heads;
@@ -153,32 +173,46 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     const uint8_t* const vh = A.cache.v + (static_cast<int64_t>(h) << shift) * D * ES;
 
     const auto base_of = [&](int32_t t) { return c0 + t * KT; };
-    // page of the tile's key `lane` (wave 0), -1 where no row sees it or there is no such page
-    const auto ask_page = [&](int32_t t) -> int32_t {
+    // Pages (wave 0): the table's entry for the tile's key `lane`, and, when it has come, what to make of it (-1 where no row
+    // sees the key or there is no such page).
+    const auto key_in = [&](int32_t t) {
         const int64_t key = static_cast<int64_t>(c0) + static_cast<int64_t>(t) * KT + lane;
-        if (key >= c1 || key < span.lo || lane >= KT) return -1;
-        const int32_t p = table[static_cast<uint32_t>(key) >> shift];
-        return p >= 0 && p < A.cache.n_pages ? p : -1;
+        return key < c1 && key >= span.lo && lane < KT;
+    };
+    const auto ask_page = [&](int32_t t) {
+        return key_in(t) ? table[static_cast<uint32_t>(c0 + t * KT + static_cast<int32_t>(lane)) >> shift] : -1;
     };
     const auto tell_page = [&](int32_t t, int32_t page) {
-        if (lane < KT) sm_page[t & 3][lane] = page;
-        const uint64_t there = __ballot(page >= 0);
+        const bool ok = key_in(t) && page >= 0 && page < A.cache.n_pages;
+        if (lane < KT) sm_page[t & 7][lane] = ok ? page : -1;
+        const uint64_t there = __ballot(ok);
         if (lane == 0) sm_there[t & 7] = there;
     };
 
+    struct Pages {
+        int32_t of[NL];  // of the thread's blocks
+        int32_t scale;
+    };
+    const auto pages_of = [&](int32_t t) {
+        Pages r;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) r.of[i] = sm_page[t & 7][(i * kThreads + tid) / CB];
+        r.scale = kE4m3 ? sm_page[t & 7][tid % KT] : 0;
+        return r;
+    };
     struct Blocks {
         Raw k[NL], v[NL];
         float scale;
         uint32_t absent;  // bit i: block i belongs to an absent key
     };
-    const auto ask = [&](int32_t t) {
+    const auto ask = [&](int32_t t, const Pages& pg) {
         Blocks r;
         r.absent = 0;
         r.scale = 0.0f;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const uint32_t at = i * kThreads + tid, row_at = at / CB, cb = at % CB;
-            const int32_t page = sm_page[t & 3][row_at];
+            const int32_t page = pg.of[i];
             if (page < 0) r.absent |= 1u << i;
             const uint32_t in = ((static_cast<uint32_t>(base_of(t)) + row_at) & in_page) * D + cb * 8u;
             const int64_t p0 = max(page, 0);
@@ -188,7 +222,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
         if constexpr (kE4m3) {
             if (tid < 2u * KT) {
                 const uint32_t row_at = tid % KT;
-                const int32_t page = sm_page[t & 3][row_at];
+                const int32_t page = pg.scale;
                 const uint32_t in = (static_cast<uint32_t>(base_of(t)) + row_at) & in_page;
                 const float* from = tid < KT ? A.cache.k_scale : A.cache.v_scale;
                 r.scale = from[((static_cast<int64_t>(max(page, 0)) * heads + h) << shift) + in];
@@ -255,14 +289,14 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
             for (int f = 0; f < FB; ++f) o[f] = P::mfma32(values(t, st, f), pw[st], o[f]);
     };
     constexpr uint64_t kAll = KT == 64 ? ~uint64_t(0) : (uint64_t(1) << (KT & 63)) - 1u;
-    const auto seen_of = [&](int32_t t) {  // the tile's keys that this lane's row sees
+    const auto seen_of = [&](int32_t t, uint64_t there) {  // the tile's keys that this lane's row sees
         const int32_t base = base_of(t);
         const int32_t lo = min(max(see_lo - base, 0), KT), hi = min(max(pos + 1 - base, 0), KT);
         const uint64_t below = lo >= 64 ? 0u : ~uint64_t(0) << lo, above = hi >= 64 ? 0u : ~uint64_t(0) << hi;
-        return sm_there[t & 7] & below & ~above;
+        return there & below & ~above;
     };
     // scores to P; the sums follow the reference
-    const auto softmax = [&](int32_t t) {
+    const auto softmax = [&](int32_t t, uint64_t there) {
         if constexpr (kE4m3) {
 #pragma unroll
             for (int b = 0; b < TB; ++b)
@@ -274,10 +308,10 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
                 }
         }
         const int32_t base = base_of(t);
-        const bool whole = base >= wlast_row.lo && base + KT <= wfirst_row.hi && sm_there[t & 7] == kAll;
+        const bool whole = base >= wlast_row.lo && base + KT <= wfirst_row.hi && there == kAll;
         uint64_t seen = kAll;
         if (!whole) {
-            seen = seen_of(t);
+            seen = seen_of(t, there);
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
                 const uint32_t bits = static_cast<uint32_t>(seen >> (32 * b)) >> (4u * g);
@@ -335,6 +369,12 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
 #pragma unroll
             for (int j = 0; j < 4; ++j) pw[st][j] = P::pack(s[st / 2][8 * (st % 2) + 2 * j], s[st / 2][8 * (st % 2) + 2 * j + 1]);
     };
+    const auto there_of = [&](int32_t t) { return sm_there[t & 7]; };
+    const auto same = [](uint64_t x) {  // for all lanes
+        const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+        const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+        return static_cast<uint64_t>(hi) << 32 | lo;
+    };
     // the end of a phase: what it wrote to LDS is there, and nothing moves across
     const auto phase = [&]() {
         __builtin_amdgcn_sched_barrier(0);
@@ -349,43 +389,54 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     // put in turn t is first read in turn t + 2, by when both halves have put their blocks.
     if (n_tiles > 0) {
         Blocks blocks;
-        int32_t page = -1;  // of a tile whose places are not yet free
+        Pages pages;
+        int32_t entry = -1;  // of a tile whose pages are not yet told
         if (wave == 0) {
-            const int32_t p0 = ask_page(0), p1 = ask_page(1), p2 = ask_page(2), p3 = ask_page(3);
-            page = ask_page(4);
-            tell_page(0, p0);
-            tell_page(1, p1);
-            tell_page(2, p2);
-            tell_page(3, p3);
+            int32_t e[5];
+#pragma unroll
+            for (int t = 0; t < 5; ++t) e[t] = ask_page(t);
+            entry = ask_page(5);
+#pragma unroll
+            for (int t = 0; t < 5; ++t) tell_page(t, e[t]);
         }
         phase();
         {
-            const Blocks b0 = ask(0), b1 = ask(1);
-            blocks = ask(2);
+            const Blocks b0 = ask(0, pages_of(0)), b1 = ask(1, pages_of(1));
+            blocks = ask(2, pages_of(2));
+            pages = pages_of(3);
             put(0, b0);
             put(1, b1);
         }
+        uint64_t there = there_of(0);  // each of these is read a turn before it is used
         phase();
         const auto bring = [&](int32_t t) {  // tile t into LDS, the next into registers
             if (t >= n_tiles) return;
             put(t, blocks);
-            if (t + 1 < n_tiles) blocks = ask(t + 1);
+            if (t + 1 < n_tiles) {
+                blocks = ask(t + 1, pages);
+                pages = pages_of(t + 2);
+            }
             if (wave == 0) {
-                tell_page(t + 2, page);
-                page = ask_page(t + 3);
+                tell_page(t + 3, entry);
+                entry = ask_page(t + 4);
             }
         };
         if (wave >= kWaves / 2) phase();
         scores(0);
         phase();
-        softmax(0);
+        uint64_t now = same(there);
+        there = there_of(1);
+        softmax(0, now);
         bring(2);
         phase();
         for (int32_t t = 0; t + 1 < n_tiles; ++t) {
             scores(t + 1);
             sums(t);
+            products_in_order<CH * TB, KT / 16 * FB>();
             phase();
-            softmax(t + 1);
+            now = same(there);
+            there = there_of(t + 2);
+            softmax(t + 1, now);
             bring(t + 3);
             phase();
         }
@@ -411,12 +462,13 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
         for (int32_t t = 0; t < n_tiles; ++t) {
             if (wave == 0) tell_page(t, ask_page(t));
             phase();
-            put(t, ask(t));
+            put(t, ask(t, pages_of(t)));
             phase();
             {
                 scores(t);
-                softmax(t);
-                const uint64_t seen = seen_of(t);
+                const uint64_t there = same(there_of(t));
+                softmax(t, there);
+                const uint64_t seen = seen_of(t, there);
 #pragma unroll
                 for (int st = 0; st < KT / 16; ++st) {
                     const uint32_t bits = static_cast<uint32_t>(seen >> (16 * st + 4u * g));  // keys 0..3 and 8..11 of these
