@@ -139,25 +139,32 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs A, ui
     const uint32_t rb = A.rotary / 16u;
     const bool il = A.interleaved != 0, turns = j < rb;
     const Blocks b = blocks_of(j, rb);
+    const uint32_t total = A.heads[0] + A.heads[1];
+    // a row is asked for before the cosines are made, or the row before it is done
+    u32x4v next[2];
+    const auto ask = [&](uint32_t it) {
+        const uint32_t row = (chunk * iters + it) * RPW + lane / LPH;
+        next[0] = next[1] = u32x4v{0u, 0u, 0u, 0u};
+        if (row >= total) return;
+        const uint32_t which = row < A.heads[0] ? 0u : 1u, head = which ? row - A.heads[0] : row;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(which ? A.src[1] : A.src[0]) +
+                              tok * (which ? A.src_tok[1] : A.src_tok[0]) +
+                              head * (which ? A.src_head[1] : A.src_head[0]);
+        next[0] = *reinterpret_cast<const u32x4v*>(src + b.b0 * 8u);
+        next[1] = *reinterpret_cast<const u32x4v*>(src + b.b1 * 8u);
+    };
+    ask(0);
     Turn t;
     if (rb) t = load_turn<D>(A.inv_freq, A.positions[tok], j, rb, il, sm_cs[threadIdx.x >> 6]);
-    const uint32_t total = A.heads[0] + A.heads[1];
     for (uint32_t it = 0; it < iters; ++it) {
         const uint32_t row = (chunk * iters + it) * RPW + lane / LPH;
         const bool live = row < total;
         const uint32_t which = row < A.heads[0] ? 0u : 1u;
         const uint32_t head = which ? row - A.heads[0] : row;
         float x[16];
-        if (live) {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(which ? A.src[1] : A.src[0]) +
-                                  tok * (which ? A.src_tok[1] : A.src_tok[0]) +
-                                  head * (which ? A.src_head[1] : A.src_head[0]);
-            unpack8<T>(*reinterpret_cast<const u32x4v*>(src + b.b0 * 8u), x);
-            unpack8<T>(*reinterpret_cast<const u32x4v*>(src + b.b1 * 8u), x + 8);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-        }
+        unpack8<T>(next[0], x);
+        unpack8<T>(next[1], x + 8);
+        if (it + 1 < iters) ask(it + 1);
         const uint16_t* wp = reinterpret_cast<const uint16_t*>(which ? A.weight[1] : A.weight[0]);
         if (wp) {  // the same for all lanes of a row
             float w[16];
@@ -218,17 +225,34 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs A, uint32_
     const uint32_t tok = tok_base + of_launch;
     if (tok >= tok_end) return;
     const int64_t slot = A.slots[tok];
-    // padding (negative) and slots past the pool are skipped
-    if (slot < 0 || (slot >> A.cache.page_shift) >= A.cache.n_pages) return;
-    const int64_t page = slot >> A.cache.page_shift;
-    const uint32_t at = static_cast<uint32_t>(slot) & ((1u << A.cache.page_shift) - 1u);
     const uint32_t lane = threadIdx.x & 63u, j = lane & (LPH - 1u);
     const uint32_t rb = A.rotary / 16u;
     const bool il = A.interleaved != 0, turns = j < rb;
     const Blocks b = blocks_of(j, rb);
+    const uint32_t heads = A.cache.n_kv_heads, total = 2u * heads;
+    u32x4v next[2];
+    const auto ask = [&](uint32_t it) {
+        const uint32_t row = (chunk * iters + it) * RPW + lane / LPH;
+        next[0] = next[1] = u32x4v{0u, 0u, 0u, 0u};
+        if (row >= total) return;
+        const uint32_t which = row < heads ? 0u : 1u, head = which ? row - heads : row;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(which ? A.src[1] : A.src[0]) +
+                              tok * (which ? A.src_tok[1] : A.src_tok[0]) +
+                              head * (which ? A.src_head[1] : A.src_head[0]);
+        next[0] = *reinterpret_cast<const u32x4v*>(src + b.b0 * 8u);
+        next[1] = *reinterpret_cast<const u32x4v*>(src + b.b1 * 8u);
+    };
+    // A row is asked for before its token's place is known and the cosines are
+    // made, or the row before it is done.  Codes take more registers: there a
+    // row in flight costs a wave of each SIMD (9.4 us for 8.4 at 8,191 tokens
+    // of 4 heads of 128 with it), so that it is asked for in its turn.
+    if (!kE4m3) ask(0);
+    // padding (negative) and slots past the pool are skipped
+    if (slot < 0 || (slot >> A.cache.page_shift) >= A.cache.n_pages) return;
+    const int64_t page = slot >> A.cache.page_shift;
+    const uint32_t at = static_cast<uint32_t>(slot) & ((1u << A.cache.page_shift) - 1u);
     Turn t;
     if (rb) t = load_turn<D>(A.inv_freq, A.positions[tok], j, rb, il, sm_cs[threadIdx.x >> 6]);
-    const uint32_t heads = A.cache.n_kv_heads, total = 2u * heads;
     float w[16];
     if (A.weight) {
         const uint16_t* wp = reinterpret_cast<const uint16_t*>(A.weight);
@@ -240,14 +264,9 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs A, uint32_
         const bool live = row < total;
         const uint32_t which = row < heads ? 0u : 1u;
         const uint32_t head = which ? row - heads : row;
-        u32x4v r0 = {0u, 0u, 0u, 0u}, r1 = r0;
-        if (live) {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(which ? A.src[1] : A.src[0]) +
-                                  tok * (which ? A.src_tok[1] : A.src_tok[0]) +
-                                  head * (which ? A.src_head[1] : A.src_head[0]);
-            r0 = *reinterpret_cast<const u32x4v*>(src + b.b0 * 8u);
-            r1 = *reinterpret_cast<const u32x4v*>(src + b.b1 * 8u);
-        }
+        if (kE4m3) ask(it);
+        u32x4v r0 = next[0], r1 = next[1];
+        if (!kE4m3 && it + 1 < iters) ask(it + 1);
         float x[16];
         unpack8<T>(r0, x);
         unpack8<T>(r1, x + 8);

@@ -42,6 +42,12 @@ struct AttentionArgs {
     float scale_log2;        // scale * log2(e)
 };
 
+// A word that no kernel writes meanwhile, at an address that is the same for all lanes: by way of the scalar cache, so
+// that waiting for it does not wait for the keys and values that were requested before it.
+__device__ __forceinline__ int32_t load_scalar(const int32_t* p) {
+    return *(const __attribute__((address_space(4))) int32_t*)(p);
+}
+
 // One request as a launch sees it.  Lengths are bounded by what exists, so
 // that no value of cu_q or kv_len leads outside of the buffers.
 struct Request {
@@ -132,7 +138,7 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& A, const Request& r
 }
 
 constexpr uint32_t kRowsTile = 16;   // rows of a tile in paged_rows.hip
-constexpr uint32_t kTileRows = 256;  // and in paged_tile.hip
+constexpr uint32_t tile_rows(uint32_t dim) { return dim == 256 ? 128u : 256u; }  // and in paged_tile.hip
 constexpr int32_t kRowsBlock = 128;  // keys that a workgroup of paged_rows.hip takes at a time
 constexpr int32_t kTileAlign = 64;   // a split's keys begin at a multiple of this many in paged_tile.hip
 

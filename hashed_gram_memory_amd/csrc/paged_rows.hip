@@ -55,12 +55,6 @@ __device__ __forceinline__ AttentionArgs args_anew(const AttentionArgs& args) {
 #endif
 }
 
-// A word that no kernel writes meanwhile, at an address that is the same for all lanes: by way of the scalar cache, so
-// that waiting for it does not wait for the keys and values that were requested before it.
-__device__ __forceinline__ int32_t load_scalar(const int32_t* p) {
-    return *(const __attribute__((address_space(4))) int32_t*)(p);
-}
-
 // kBytes of a row in a lane, held as one value: taken apart into words, it
 // would be copied where paths join.
 template <int kBytes>

@@ -8,13 +8,10 @@
 // at a row's first keys and hardly ever later.  The work is the two products:
 // bound by the matrix pipes, and next to them by the exponentials.
 //
-// Mapping (gfx950, wave64): a workgroup takes kWaves * 32 rows of one KV head,
-// and one split of their keys; each wave holds 32 rows' q, scores and sums in
-// registers.  K and V go through LDS, a tile of KT keys at a time, in two
-// buffers: the next tile is requested into registers before the products of
-// this one and written to LDS after them, one barrier a tile.  Registers in
-// between let the rows of absent keys be zeroed and e4m3 codes be decoded on
-// the way.
+// Mapping (gfx950, wave64): a workgroup takes 256 rows of one KV head (head_dim
+// 256: 128 rows) and one split of their keys; each wave holds 32 rows' q,
+// scores and sums in registers.  K and V go through LDS, a tile of KT keys at a
+// time, in rings of four and five buffers.
 //   * S^T = K Q^T on 32x32x16 MFMA: a lane holds a row and 16 of 32 keys, so
 //     the maximum and sum of a row need one exchange between a wave's halves,
 //     and the scores are the second product's B operand as they stand: P never
@@ -23,18 +20,38 @@
 //     reads give four keys of a channel to a lane.
 //   * 16-byte blocks of a key's row are swapped within its LDS row (K by the
 //     key's low bits, V by two of them), so that neither kind of read has two
-//     lanes on one bank.
+//     lanes on one bank.  A lane asks for the block that belongs to its place,
+//     so the swap costs nothing.
+//   * 16-bit tiles go from memory to LDS without a register between, three
+//     turns before they are read; e4m3 codes by way of registers, where they
+//     are widened (exactly).  Addresses come from the page table by scalar
+//     loads, a turn early.
+//   * Eight waves are two on each SIMD, in two halves that take turns: one does
+//     the products of a tile while the other does its softmax and asks for
+//     tiles, so that the matrix pipe and the vector pipe of a SIMD both work.
+//     A head_dim of 256 leaves registers for one wave on a SIMD: no turns.
+//
+// What it measured, for 2,048 tokens at the end of 32,768 keys, 32 heads over 8
+// of head_dim 128, bf16: 1,314 us with two buffers, staged through registers,
+// and no turns; 1,050 to 1,100 us as it stands, 1.01 PFLOP/s at the most, where
+// a product of 8192^3 reached 1.25 to 1.37 on the same card.  A turn's products
+// take 1,900 cycles of a wave for 1,190 that they take alone: LDS answers
+// products and the other half's softmax issues between them.  Of the time,
+// about a sixth is the card's power: zeros for q, K and V run that much faster.
+//
 // P is rounded once to 16 bits (bf16: half a step is 2^-9 of each p; its
 // average over the keys adds to the output about what the output's own
 // rounding does).  Twice the digits, as in paged_rows.hip, would cost half as
 // many products again, and here the products are what is waited for.
 //
 // What a row does not see: scores of hidden keys become -inf before the
-// maximum; keys that no row sees (past the end, before the window, on a page
-// outside the pool) have zeros for V.  Where a tile that only some rows see
-// in full holds infinities or NaN in V, they are replaced by zeros too, and
-// counted for the rows that see them by two more products, of ones (not below
-// +inf, not above -inf), so that no row meets a value that its mask hides.
+// maximum, and their p is 0.  A key that no row sees (past the end, before the
+// window) is read from one that some row sees, and one on a page outside the
+// pool as zeros, so nothing is read that is not the request's.  Keys that only
+// some rows see can hold infinities or NaN in V, and 0 times them is NaN: where
+// a workgroup's sums end with a NaN, it takes its keys again with zeros in the
+// places of infinities and NaN, and counts those for the rows that see them by
+// two more products, of ones (not below +inf, not above -inf).
 #include <type_traits>
 
 #include "paged_attention.h"
@@ -44,11 +61,12 @@ namespace {
 
 typedef short s16x4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4v lds_s16x4v;
+typedef __attribute__((address_space(3))) const u32x4v lds_u32x4v;
 
 // Block (16 bytes of 16-bit channels) of a key's LDS row where channel block c lies.
 template <int D>
 __device__ __forceinline__ uint32_t k_block(uint32_t key, uint32_t c) {
-    return D == 64 ? c ^ ((key >> 1) & 7u) : c ^ (key & 15u);
+    return c ^ (D == 64 ? (key >> 1) & 7u : D == 128 ? key & 15u : key & 7u);
 }
 template <int D>
 __device__ __forceinline__ uint32_t v_block(uint32_t key, uint32_t c) {
@@ -75,6 +93,28 @@ __device__ __forceinline__ void products_in_order() {
     __builtin_amdgcn_sched_group_barrier(kMfma, kAhead, 0);
 }
 
+// What the rows of pages that are none are read from.
+__device__ __attribute__((aligned(16))) const uint8_t g_zeros[4096] = {};
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)(p)));
+}
+// 16 bytes of each lane to LDS, lane after lane from an address that is the same for all.  The compiler knows of no such
+// load: wait_loads is to stand between it and the barrier that its readers wait for.  M0 holds the LDS address; nothing
+// else in this kernel uses it.
+__device__ __forceinline__ void to_lds(uint64_t base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(offset), "s"(base), "s"(to)
+                 : "memory");
+}
+// all but the last kMost loads have come
+template <int kMost>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kMost) : "memory");
+}
+
 // eight e4m3 codes as 16-bit numbers
 template <class T>
 __device__ __forceinline__ u32x4v widen(u32x2v w) {
@@ -83,9 +123,10 @@ __device__ __forceinline__ u32x4v widen(u32x2v w) {
 }
 
 template <class T, int D, bool kE4m3, int kWaves>
-__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void paged_tile_kernel(
+__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(kWaves / 4, kWaves / 4))) void paged_tile_kernel(
     const AttentionArgs A) {
     constexpr uint32_t kRows = kWaves * 32u, kThreads = kWaves * 64u;
+    constexpr bool kTurns = kWaves == 8;            // two waves on a SIMD
     constexpr int KT = D == 256 ? 32 : 64;          // keys of a tile
     constexpr int TB = KT / 32;                     // blocks of 32 keys
     constexpr int CB = D / 8;                       // 16-byte blocks of a row
@@ -94,15 +135,12 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     constexpr int NL = KT * CB / int(kThreads);     // blocks of K (and of V) that a thread brings
     static_assert(NL >= 1 && NL * int(kThreads) == KT * CB, "every thread brings the same");
     using P = std::conditional_t<kE4m3, Bf16, T>;   // P and V's type; e4m3 codes are exact in both types
-    using Raw = std::conditional_t<kE4m3, u32x2v, u32x4v>;
     constexpr uint32_t ES = kE4m3 ? 1 : 2;
     constexpr float kSlack = P::kSlack, kShift = P::kShift;
 
-    __shared__ __attribute__((aligned(1024))) uint16_t sm_k[3][KT * D];
-    __shared__ __attribute__((aligned(1024))) uint16_t sm_v[4][KT * D];
-    __shared__ __attribute__((aligned(16))) float sm_scale[4][2][kE4m3 ? KT : 4];
-    __shared__ int32_t sm_page[8][KT];       // page of each key, -1: absent
-    __shared__ uint64_t sm_there[8];         // keys that are there, by bit
+    __shared__ __attribute__((aligned(1024))) uint16_t sm_k[4][KT * D];
+    __shared__ __attribute__((aligned(1024))) uint16_t sm_v[5][KT * D];
+    __shared__ __attribute__((aligned(16))) float sm_scale[8][2][kE4m3 ? KT : 4];
 
     const uint32_t heads = A.cache.n_kv_heads;
     const uint32_t tile_at = blockIdx.x / heads, h = blockIdx.x - tile_at * heads;
@@ -115,7 +153,6 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     const uint32_t row0 = ((rows - 1u) / kRows) * kRows - tile.row0;
     const uint32_t n_rows = min(kRows, rows - row0);
     const Span span = span_of(A, req, row0, n_rows);
-    const Span first_row = span_of(A, req, row0, 1), last_row = span_of(A, req, row0 + n_rows - 1u, 1);
 
     // this split's keys [c0, c1)
     const int32_t base0 = span.lo & ~(kTileAlign - 1);
@@ -130,7 +167,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     } else if (split != 0) {
         return;
     }
-    const int32_t n_tiles = (c1 - c0 + KT - 1) / KT;
+    const int32_t n_tiles = static_cast<int32_t>((static_cast<uint32_t>(c1 - c0) + KT - 1u) / KT);
 
     const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63u;
     const uint32_t n = lane & 31u, g = lane >> 5;
@@ -173,145 +210,177 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
     const uint8_t* const vh = A.cache.v + (static_cast<int64_t>(h) << shift) * D * ES;
 
     const auto base_of = [&](int32_t t) { return c0 + t * KT; };
-    // Pages (wave 0): the table's entry for the tile's key `lane`, and, when it has come, what to make of it (-1 where no row
-    // sees the key or there is no such page).
-    const auto key_in = [&](int32_t t) {
-        const int64_t key = static_cast<int64_t>(c0) + static_cast<int64_t>(t) * KT + lane;
-        return key < c1 && key >= span.lo && lane < KT;
-    };
-    const auto ask_page = [&](int32_t t) {
-        return key_in(t) ? table[static_cast<uint32_t>(c0 + t * KT + static_cast<int32_t>(lane)) >> shift] : -1;
-    };
-    const auto tell_page = [&](int32_t t, int32_t page) {
-        const bool ok = key_in(t) && page >= 0 && page < A.cache.n_pages;
-        if (lane < KT) sm_page[t & 7][lane] = ok ? page : -1;
-        const uint64_t there = __ballot(ok);
-        if (lane == 0) sm_there[t & 7] = there;
-    };
-
+    // A thread brings the blocks at the LDS places i * kThreads + tid of a tile.  A wave's blocks i are those of 64 / CB rows
+    // within one run of 8 keys, and so on one page: their address is the same for all lanes but for a constant.
+    constexpr uint32_t kStep = kThreads / CB;  // rows from one i to the next: blocks are swapped alike in them
+    static_assert(kStep % (D == 256 ? 8 : 16) == 0, "");
+    const uint32_t wave_row = wave * (64u / CB);
+    const uint32_t k_col = k_block<D>(tid / CB, tid % CB) * 8u * ES, v_col = v_block<D>(tid / CB, tid % CB) * 8u * ES;
     struct Pages {
-        int32_t of[NL];  // of the thread's blocks
-        int32_t scale;
+        int32_t of[NL];  // of the wave's blocks
     };
-    const auto pages_of = [&](int32_t t) {
+    // The first key of the wave's rows i, or where all of them lie outside of [span.lo, c1), of rows in the run next to them.
+    const auto key_of = [&](int32_t t, int i) __attribute__((always_inline)) {
+        const int64_t key = static_cast<int64_t>(base_of(t)) + wave_row + i * kStep;
+        const int32_t low = (span.lo & ~7) + static_cast<int32_t>(wave_row & 7u);
+        return static_cast<int32_t>(min(max(key, static_cast<int64_t>(low)), static_cast<int64_t>(c1 - 1)));
+    };
+    const auto ask_pages = [&](int32_t t) __attribute__((always_inline)) {
         Pages r;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) r.of[i] = sm_page[t & 7][(i * kThreads + tid) / CB];
-        r.scale = kE4m3 ? sm_page[t & 7][tid % KT] : 0;
+        for (int i = 0; i < NL; ++i) r.of[i] = load_scalar(table + (static_cast<uint32_t>(key_of(t, i)) >> shift));
         return r;
     };
+    // Where the wave's blocks come from: one address, and what each lane adds to it.  A key that no row sees takes the row of
+    // one that some row sees: its weight is 0.
+    struct Source {
+        uint64_t k, v;
+        uint32_t k_off, v_off;
+    };
+    struct Sources {
+        Source of[NL];
+    };
+    const auto sources_of = [&](int32_t t, const Pages& pg) __attribute__((always_inline)) {
+        Sources r;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int32_t key = key_of(t, i);
+            const uint32_t in = static_cast<uint32_t>(key) & in_page;
+            const int64_t p = pg.of[i];
+            const bool ok = p >= 0 && p < A.cache.n_pages;
+            const uint64_t none = reinterpret_cast<uint64_t>(g_zeros);
+            r.of[i].k = ok ? reinterpret_cast<uint64_t>(kh + (p * A.cache.k_page_stride + in * D) * ES) : none;
+            r.of[i].v = ok ? reinterpret_cast<uint64_t>(vh + (p * A.cache.v_page_stride + in * D) * ES) : none;
+            const int32_t more = min(max(static_cast<int32_t>(lane / CB), span.lo - key), c1 - 1 - key);
+            r.of[i].k_off = static_cast<uint32_t>(more) * (D * ES) + k_col;
+            r.of[i].v_off = static_cast<uint32_t>(more) * (D * ES) + v_col;
+        }
+        return r;
+    };
+    // 16 bits: straight to LDS
+    const auto fetch = [&](int32_t t, const Sources& from) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const uint32_t at = wave * 1024u + i * kThreads * 16u;
+            to_lds(from.of[i].k, from.of[i].k_off, at + lds_address(&sm_k[t & 3][0]));
+            to_lds(from.of[i].v, from.of[i].v_off, at + lds_address(&sm_v[static_cast<uint32_t>(t) % 5u][0]));
+        }
+    };
+    // e4m3: by way of registers, to be widened
     struct Blocks {
-        Raw k[NL], v[NL];
-        float scale;
-        uint32_t absent;  // bit i: block i belongs to an absent key
+        u32x2v k[NL], v[NL];
     };
-    const auto ask = [&](int32_t t, const Pages& pg) {
+    const auto ask = [&](const Sources& from) __attribute__((always_inline)) {
         Blocks r;
-        r.absent = 0;
-        r.scale = 0.0f;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const uint32_t at = i * kThreads + tid, row_at = at / CB, cb = at % CB;
-            const int32_t page = pg.of[i];
-            if (page < 0) r.absent |= 1u << i;
-            const uint32_t in = ((static_cast<uint32_t>(base_of(t)) + row_at) & in_page) * D + cb * 8u;
-            const int64_t p0 = max(page, 0);
-            r.k[i] = *reinterpret_cast<const Raw*>(kh + (p0 * A.cache.k_page_stride + in) * ES);
-            r.v[i] = *reinterpret_cast<const Raw*>(vh + (p0 * A.cache.v_page_stride + in) * ES);
-        }
-        if constexpr (kE4m3) {
-            if (tid < 2u * KT) {
-                const uint32_t row_at = tid % KT;
-                const int32_t page = pg.scale;
-                const uint32_t in = (static_cast<uint32_t>(base_of(t)) + row_at) & in_page;
-                const float* from = tid < KT ? A.cache.k_scale : A.cache.v_scale;
-                r.scale = from[((static_cast<int64_t>(max(page, 0)) * heads + h) << shift) + in];
-                if (page < 0) r.scale = 0.0f;
-            }
+            r.k[i] = *reinterpret_cast<const u32x2v*>(from.of[i].k + from.of[i].k_off);
+            r.v[i] = *reinterpret_cast<const u32x2v*>(from.of[i].v + from.of[i].v_off);
         }
         return r;
     };
-    const auto put = [&](int32_t t, const Blocks& r) {
-        const uint32_t kt = static_cast<uint32_t>(t) % 3u;
+    const auto put = [&](int32_t t, const Blocks& r) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const uint32_t at = i * kThreads + tid, row_at = at / CB, cb = at % CB;
-            u32x4v kw, vw;
-            if constexpr (kE4m3) {
-                kw = widen<T>(r.k[i]);
-                vw = widen<P>(r.v[i]);
-            } else {
-                kw = r.k[i];
-                vw = r.v[i];
-            }
-            if ((r.absent >> i) & 1u) vw = u32x4v{0u, 0u, 0u, 0u};
-            *reinterpret_cast<u32x4v*>(&sm_k[kt][row_at * D + k_block<D>(row_at, cb) * 8u]) = kw;
-            *reinterpret_cast<u32x4v*>(&sm_v[t & 3][row_at * D + v_block<D>(row_at, cb) * 8u]) = vw;
+            const uint32_t at = (i * kThreads + tid) * 8u;
+            *reinterpret_cast<u32x4v*>(&sm_k[t & 3][at]) = widen<T>(r.k[i]);
+            *reinterpret_cast<u32x4v*>(&sm_v[static_cast<uint32_t>(t) % 5u][at]) = widen<P>(r.v[i]);
         }
-        if constexpr (kE4m3) {
-            if (tid < 2u * KT) sm_scale[t & 3][tid / KT][tid % KT] = r.scale;
-        }
+    };
+    // the scale of key tid % KT: of K (tid < KT), of V
+    const auto ask_scale_page = [&](int32_t t) __attribute__((always_inline)) {
+        const int64_t key = min(static_cast<int64_t>(base_of(t)) + tid % KT, static_cast<int64_t>(c1) - 1);
+        return tid < 2u * KT ? table[static_cast<uint32_t>(key) >> shift] : -1;
+    };
+    const auto ask_scale = [&](int32_t t, int32_t page) __attribute__((always_inline)) {
+        const uint32_t in = (static_cast<uint32_t>(base_of(t)) + tid % KT) & in_page;
+        const float* from = tid < KT ? A.cache.k_scale : A.cache.v_scale;
+        const bool ok = page >= 0 && page < A.cache.n_pages;
+        return ok ? from[((static_cast<int64_t>(page) * heads + h) << shift) + in] : 0.0f;
+    };
+    const auto put_scale = [&](int32_t t, float x) __attribute__((always_inline)) {
+        if (tid < 2u * KT) sm_scale[t & 7][tid / KT][tid % KT] = x;
     };
 
+    bool all_there = true;  // all pages: else every tile is looked at as one that a mask cuts
     f32x16v s[TB];       // scores, then softmax terms
     u32x4v pw[KT / 16];  // P in 16 bits
+    // LDS places that a lane reads, in a tile's buffer: constant, so that a buffer's turn costs one addition for each
+    uint32_t k_at[CH], v_at[FB];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) k_at[i] = (n * D + k_block<D>(n, 2 * i + g) * 8u) * 2u;
+    {
+        const uint32_t z = lane & 15u;  // of 16 lanes that read 4 keys of 16 channels
+        const uint32_t row_at = 4u * g + (z >> 2), col = 2u * ((lane >> 4) & 1u) + ((z & 3u) >> 1);
+#pragma unroll
+        for (int f = 0; f < FB; ++f) v_at[f] = (row_at * D + v_block<D>(row_at, 4 * f + col) * 8u + 4u * (z & 1u)) * 2u;
+    }
     // S^T = K Q^T
-    const auto scores = [&](int32_t t) {
-        const uint16_t* kb = sm_k[static_cast<uint32_t>(t) % 3u];
+    const auto scores = [&](int32_t t) __attribute__((always_inline)) {
+        const uint32_t from = lds_address(&sm_k[t & 3][0]);
 #pragma unroll
         for (int b = 0; b < TB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
+        for (int i = 0; i < CH; ++i) {
+            const uint32_t at = from + k_at[i];
 #pragma unroll
-            for (int b = 0; b < TB; ++b) {
-                const u32x4v a = *reinterpret_cast<const u32x4v*>(&kb[(32 * b + n) * D + k_block<D>(n, 2 * i + g) * 8u]);
-                s[b] = T::mfma32(a, q[i], s[b]);
-            }
+            for (int b = 0; b < TB; ++b)
+                s[b] = T::mfma32(*reinterpret_cast<lds_u32x4v*>(at + 32u * b * D * 2u), q[i], s[b]);
+        }
     };
     // V's channels 32 f + n at the keys 16 st + 4g + 0..3 and 8 more; v_block takes the key's bits 0 and 1 only
-    const auto values = [&](int32_t t, int st, int f) {
-        const uint16_t* vb = sm_v[t & 3];
-        const uint32_t z = lane & 15u;  // of 16 lanes that read 4 keys of 16 channels
-        const uint32_t vrow = 4u * g + (z >> 2), vcol = 2u * ((lane >> 4) & 1u) + ((z & 3u) >> 1);
-        const uint32_t at = (16 * st + vrow) * D + v_block<D>(vrow, 4 * f + vcol) * 8u + 4u * (z & 1u);
-        const s16x4v x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at]);
-        const s16x4v x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4v*)&vb[at + 8 * D]);
+    const auto values = [&](uint32_t at, int st) __attribute__((always_inline)) {
+        const s16x4v x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4v*>(at + 16u * st * D * 2u));
+        const s16x4v x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4v*>(at + (16u * st + 8u) * D * 2u));
         const u32x2v w0 = __builtin_bit_cast(u32x2v, x0), w1 = __builtin_bit_cast(u32x2v, x1);
         return u32x4v{w0[0], w0[1], w1[0], w1[1]};
     };
     // O^T += V^T P^T
-    const auto sums = [&](int32_t t) {
+    const auto sums = [&](int32_t t) __attribute__((always_inline)) {
+        const uint32_t from = lds_address(&sm_v[static_cast<uint32_t>(t) % 5u][0]);
+        uint32_t at[FB];
+#pragma unroll
+        for (int f = 0; f < FB; ++f) at[f] = from + v_at[f];
 #pragma unroll
         for (int st = 0; st < KT / 16; ++st)
 #pragma unroll
-            for (int f = 0; f < FB; ++f) o[f] = P::mfma32(values(t, st, f), pw[st], o[f]);
+            for (int f = 0; f < FB; ++f) o[f] = P::mfma32(values(at[f], st), pw[st], o[f]);
     };
-    constexpr uint64_t kAll = KT == 64 ? ~uint64_t(0) : (uint64_t(1) << (KT & 63)) - 1u;
-    const auto seen_of = [&](int32_t t, uint64_t there) {  // the tile's keys that this lane's row sees
+    const auto seen_of = [&](int32_t t) __attribute__((always_inline)) {  // the tile's keys that this lane's row sees
         const int32_t base = base_of(t);
-        const int32_t lo = min(max(see_lo - base, 0), KT), hi = min(max(pos + 1 - base, 0), KT);
+        const int32_t lo = min(max(see_lo - base, 0), KT), hi = min(max(min(pos + 1, c1) - base, 0), KT);
         const uint64_t below = lo >= 64 ? 0u : ~uint64_t(0) << lo, above = hi >= 64 ? 0u : ~uint64_t(0) << hi;
-        return there & below & ~above;
+        uint64_t seen = below & ~above;
+        if (!all_there) {
+#pragma unroll
+            for (int i = 0; i < KT / 8; ++i) {
+                const uint32_t key = min(static_cast<uint32_t>(base) + 8u * i, static_cast<uint32_t>(c1) - 1u);
+                const int32_t p = load_scalar(table + (key >> shift));
+                if (p < 0 || p >= A.cache.n_pages) seen &= ~(uint64_t(0xFF) << (8 * i));
+            }
+        }
+        return seen;
     };
     // scores to P; the sums follow the reference
-    const auto softmax = [&](int32_t t, uint64_t there) {
+    const auto softmax = [&](int32_t t) __attribute__((always_inline)) {
         if constexpr (kE4m3) {
 #pragma unroll
             for (int b = 0; b < TB; ++b)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const f32x4v ks = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 3][0][32 * b + 8 * y + 4 * g]);
+                    const f32x4v ks = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 7][0][32 * b + 8 * y + 4 * g]);
 #pragma unroll
                     for (int z = 0; z < 4; ++z) s[b][4 * y + z] *= ks[z];
                 }
         }
         const int32_t base = base_of(t);
-        const bool whole = base >= wlast_row.lo && base + KT <= wfirst_row.hi && there == kAll;
-        uint64_t seen = kAll;
+        // tiles end where a split's keys do, or a row's
+        const bool whole = base >= wlast_row.lo && base + KT <= wfirst_row.hi && all_there;
+        uint64_t seen = ~uint64_t(0);
         if (!whole) {
-            seen = seen_of(t, there);
+            seen = seen_of(t);
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
                 const uint32_t bits = static_cast<uint32_t>(seen >> (32 * b)) >> (4u * g);
@@ -351,7 +420,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
             for (int b = 0; b < TB; ++b)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const f32x4v vs = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 3][1][32 * b + 8 * y + 4 * g]);
+                    const f32x4v vs = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 7][1][32 * b + 8 * y + 4 * g]);
 #pragma unroll
                     for (int z = 0; z < 4; ++z) s[b][4 * y + z] *= vs[z];
                 }
@@ -369,14 +438,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
 #pragma unroll
             for (int j = 0; j < 4; ++j) pw[st][j] = P::pack(s[st / 2][8 * (st % 2) + 2 * j], s[st / 2][8 * (st % 2) + 2 * j + 1]);
     };
-    const auto there_of = [&](int32_t t) { return sm_there[t & 7]; };
-    const auto same = [](uint64_t x) {  // for all lanes
-        const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
-        const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
-        return static_cast<uint64_t>(hi) << 32 | lo;
-    };
     // the end of a phase: what it wrote to LDS is there, and nothing moves across
-    const auto phase = [&]() {
+    const auto phase = [&]() __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
         __builtin_amdgcn_s_barrier();
@@ -386,62 +449,76 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
 
     // Two halves of the workgroup, a wave of each on every SIMD, take turns: while one does the products of its turn t
     // (the scores of tile t + 1, the sums of tile t), the other does the softmax of its own and brings tiles.  A tile that is
-    // put in turn t is first read in turn t + 2, by when both halves have put their blocks.
+    // asked for in turn t is first read in turn t + 3.
     if (n_tiles > 0) {
+        // e4m3 has a tile in registers between, and scales a turn behind for each step
+        constexpr int kLead = kE4m3 ? 1 : 0;
         Blocks blocks;
-        Pages pages;
-        int32_t entry = -1;  // of a tile whose pages are not yet told
-        if (wave == 0) {
-            int32_t e[5];
-#pragma unroll
-            for (int t = 0; t < 5; ++t) e[t] = ask_page(t);
-            entry = ask_page(5);
-#pragma unroll
-            for (int t = 0; t < 5; ++t) tell_page(t, e[t]);
-        }
-        phase();
-        {
-            const Blocks b0 = ask(0, pages_of(0)), b1 = ask(1, pages_of(1));
-            blocks = ask(2, pages_of(2));
-            pages = pages_of(3);
+        float scale = 0.0f;
+        int32_t scale_page = -1;
+        const Sources f0 = sources_of(0, ask_pages(0)), f1 = sources_of(1, ask_pages(1)), f2 = sources_of(2, ask_pages(2));
+        if constexpr (kE4m3) {
+            const Blocks b0 = ask(f0), b1 = ask(f1), b2 = ask(f2);
+            blocks = ask(sources_of(3, ask_pages(3)));
+            put_scale(0, ask_scale(0, ask_scale_page(0)));
+            scale = ask_scale(1, ask_scale_page(1));
+            scale_page = ask_scale_page(2);
             put(0, b0);
             put(1, b1);
+            put(2, b2);
+        } else {
+            fetch(0, f0);
+            fetch(1, f1);
+            fetch(2, f2);
         }
-        uint64_t there = there_of(0);  // each of these is read a turn before it is used
+        bool bad = false;
+        for (uint32_t i = (static_cast<uint32_t>(c0) >> shift) + tid; i <= static_cast<uint32_t>(c1 - 1) >> shift; i += kThreads) {
+            const int32_t p = table[i];
+            bad |= p < 0 || p >= A.cache.n_pages;
+        }
+        all_there = !__syncthreads_or(bad);
+        if constexpr (!kE4m3) wait_loads<0>();
+        Pages pages = ask_pages(3 + kLead);
         phase();
-        const auto bring = [&](int32_t t) {  // tile t into LDS, the next into registers
-            if (t >= n_tiles) return;
-            put(t, blocks);
-            if (t + 1 < n_tiles) {
-                blocks = ask(t + 1, pages);
-                pages = pages_of(t + 2);
-            }
-            if (wave == 0) {
-                tell_page(t + 3, entry);
-                entry = ask_page(t + 4);
+        // softmax of tile t, and tile b brought; its pages were asked for a turn before, and its addresses made among the
+        // products, where a wave has instructions to spare.  Tiles past the last are brought too, and not read.
+        const auto softmax_and_bring = [&](int32_t t, int32_t b, const Sources& from) __attribute__((always_inline)) {
+            pages = ask_pages(b + 1 + kLead);
+            softmax(t);
+            if constexpr (kE4m3) {
+                put_scale(b - 2, scale);
+                scale = ask_scale(b - 1, scale_page);
+                scale_page = ask_scale_page(b);
+                put(b, blocks);
+                blocks = ask(from);
+            } else {
+                fetch(b, from);
             }
         };
-        if (wave >= kWaves / 2) phase();
+        if (kTurns && wave >= kWaves / 2) phase();
+        Sources from = sources_of(3 + kLead, pages);
         scores(0);
         phase();
-        uint64_t now = same(there);
-        there = there_of(1);
-        softmax(0, now);
-        bring(2);
+        softmax_and_bring(0, 3, from);
         phase();
         for (int32_t t = 0; t + 1 < n_tiles; ++t) {
+            __builtin_amdgcn_s_setprio(1);  // products first: they leave the other half enough of the issue slots
+            from = sources_of(t + 4 + kLead, pages);
             scores(t + 1);
             sums(t);
             products_in_order<CH * TB, KT / 16 * FB>();
+            if constexpr (!kE4m3) {  // tile t + 2 is there when both halves are past this; of tile t + 3 nothing is needed yet
+                __builtin_amdgcn_sched_barrier(0);
+                wait_loads<2 * NL>();
+            }
+            __builtin_amdgcn_s_setprio(0);
             phase();
-            now = same(there);
-            there = there_of(t + 2);
-            softmax(t + 1, now);
-            bring(t + 3);
+            softmax_and_bring(t + 1, t + 4, from);
             phase();
         }
         sums(n_tiles - 1);
-        if (wave < kWaves / 2) phase();
+        if constexpr (!kE4m3) wait_loads<0>();
+        if (kTurns && wave < kWaves / 2) phase();
     }
 
     // A NaN in the sums may be there by right, or come from 0 * infinity or 0 * NaN of a value that its row's mask hides:
@@ -460,15 +537,20 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
             for (int i = 0; i < 16; ++i) o[f][i] = 0.0f;
 #pragma unroll 1
         for (int32_t t = 0; t < n_tiles; ++t) {
-            if (wave == 0) tell_page(t, ask_page(t));
-            phase();
-            put(t, ask(t, pages_of(t)));
+            const Sources from = sources_of(t, ask_pages(t));
+            if constexpr (kE4m3) {
+                put(t, ask(from));
+                put_scale(t, ask_scale(t, ask_scale_page(t)));
+            } else {
+                fetch(t, from);
+                wait_loads<0>();
+            }
             phase();
             {
                 scores(t);
-                const uint64_t there = same(there_of(t));
-                softmax(t, there);
-                const uint64_t seen = seen_of(t, there);
+                softmax(t);
+                const uint64_t seen = seen_of(t);
+                const uint32_t at_v = lds_address(&sm_v[static_cast<uint32_t>(t) % 5u][0]);
 #pragma unroll
                 for (int st = 0; st < KT / 16; ++st) {
                     const uint32_t bits = static_cast<uint32_t>(seen >> (16 * st + 4u * g));  // keys 0..3 and 8..11 of these
@@ -477,7 +559,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
                     for (int w = 0; w < 4; ++w) one[w] = P::ones((bits >> (8 * (w / 2) + 2 * (w % 2))) & 3u);
 #pragma unroll
                     for (int f = 0; f < FB; ++f) {
-                        u32x4v a = values(t, st, f), up, down;
+                        u32x4v a = values(at_v + v_at[f], st), up, down;
                         f32x16v zero;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
@@ -533,8 +615,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 
 
 template <class T, int D, bool kE4m3>
 hipError_t tile_one(const AttentionArgs& a, hipStream_t stream) {
-    constexpr int kWaves = kTileRows / 32;
-    const dim3 grid(tile_count<kTileRows>(a) * a.cache.n_kv_heads, a.n_split);
+    constexpr int kWaves = tile_rows(D) / 32;
+    const dim3 grid(tile_count<tile_rows(D)>(a) * a.cache.n_kv_heads, a.n_split);
     hipLaunchKernelGGL((paged_tile_kernel<T, D, kE4m3, kWaves>), grid, dim3(kWaves * 64), 0, stream, a);
     return hipGetLastError();
 }

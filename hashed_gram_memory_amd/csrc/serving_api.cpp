@@ -198,11 +198,12 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     if (out->any_many) {
         AttentionArgs& m = out->many;
         m.min_rows = out->any_few ? kFewRows + 1 : 0;
-        if (!m.cu_q) m.tiles_per = static_cast<uint32_t>((most_rows + kTileRows - 1) / kTileRows);
-        const uint64_t groups = tile_count<kTileRows>(m) * heads;
+        const uint32_t of_tile = tile_rows(d->cache->head_dim);
+        if (!m.cu_q) m.tiles_per = static_cast<uint32_t>((most_rows + of_tile - 1) / of_tile);
+        const uint64_t groups = (of_tile == 128 ? tile_count<128>(m) : tile_count<256>(m)) * heads;
         if (groups > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
         const uint64_t all_rows = uint64_t(m.n_tok) * d->n_q_heads;
-        const Split s = split_tiles(groups, keys_of(kTileRows, kTileAlign), all_rows, d->cache->head_dim);
+        const Split s = split_tiles(groups, keys_of(of_tile, kTileAlign), all_rows, d->cache->head_dim);
         m.split_tokens = s.tokens;
         m.n_split = s.n;
         if (s.n > 1) {
