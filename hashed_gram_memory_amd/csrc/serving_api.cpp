@@ -65,8 +65,10 @@ struct Split {
 // Many rows (paged_tile.hip).  A workgroup fills a CU, so a launch takes
 // ceil(groups * n / 256) rounds of a split's keys, and joining writes and reads
 // n fp32 rows for each row; of up to 32 splits the one with the least of both.
+// A round took 0.020, 0.032 and 0.036 us a key for head_dim 64, 128 and 256
+// (2,048 tokens over 32,768 keys, bf16).
 Split split_tiles(uint64_t groups, int64_t most_keys, uint64_t rows, uint32_t dim) {
-    const double key_us = 4e-4 * dim, join_us = rows * dim * 8.0 / 4e6;
+    const double key_us = dim == 256 ? 0.036 : 0.008 + 1.9e-4 * dim, join_us = rows * dim * 8.0 / 4e6;
     double best = 0;
     Split s = {0u, 1u};
     for (uint32_t n = 1; n <= 32; ++n) {
@@ -201,7 +203,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         const uint32_t of_tile = tile_rows(d->cache->head_dim);
         if (!m.cu_q) m.tiles_per = static_cast<uint32_t>((most_rows + of_tile - 1) / of_tile);
         const uint64_t groups = (of_tile == 128 ? tile_count<128>(m) : tile_count<256>(m)) * heads;
-        if (groups > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
+        if (groups >= uint64_t(1) << 23) return ENGRAM_ERANGE;  // 512 threads each, and a grid has less than 2^32
         const uint64_t all_rows = uint64_t(m.n_tok) * d->n_q_heads;
         const Split s = split_tiles(groups, keys_of(of_tile, kTileAlign), all_rows, d->cache->head_dim);
         m.split_tokens = s.tokens;

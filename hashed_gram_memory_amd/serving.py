@@ -10,6 +10,8 @@ page_size] for K and V.
     kv_append(k, v, k_cache, v_cache, slots, positions=positions, inv_freq=inv_freq, k_weight=wk)  # engram_kv_append
     out = paged_attention(q, k_cache, v_cache, block_table, kv_len)       # engram_paged_attention
 
+attention_example.py runs them together, next to the lookup.
+
 The operators serve: they have no backward, and refuse tensors that require
 a gradient while gradients are recorded.  They run on the current stream of
 their tensors' device, or on ``stream``.  The calls are marshalled by the
@@ -119,7 +121,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
     Request b has tokens cu_q[b] .. cu_q[b+1]-1 (int32 [n_seq + 1]; None: equally many each) and kv_len[b] cached keys
     (int32 [n_seq]) on the pages block_table[b] (int32 [n_seq, width]).  ``max_q_len`` bounds the tokens of a request
-    where it is known.  ``scale`` defaults to head_dim ** -0.5; ``window`` > 0 lets a token see that many keys.
+    where it is known: a batch of single tokens takes fewer launches with it, and a request that is longer may be left
+    out.  ``scale`` defaults to head_dim ** -0.5; ``window`` > 0 lets a token see that many keys.
     ``workspace``: uint8 of paged_attention_workspace bytes, 256-byte aligned; allocated if not given."""
     args = (q, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, scale, window, k_scale, v_scale, out, return_lse,
             workspace, False)

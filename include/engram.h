@@ -543,7 +543,10 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  *     lse = log(sum_j exp(scale * q . k_j))            (natural)
  * A token that sees no key gets out = 0 and lse = -infinity.  What a token
  * does not see never reaches its result, NaN and infinities included.
- * Products of 16-bit operands with fp32 sums; softmax in fp32.
+ * Products of 16-bit operands with fp32 sums; softmax in fp32.  For the second
+ * product a_j is held in about 16 bits where a request has at most 32 rows (new
+ * tokens * n_q_heads / n_kv_heads), and rounded once to `type` (E4M3 caches:
+ * to BF16) where it has more.
  *
  *   lse         device fp32 [n_tok][n_q_heads], or NULL.
  *   block_table device int32 [n_seq][table_width], rows table_stride apart.  A
@@ -551,7 +554,9 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  *               as unseen.  kv_len is bounded by table_width * page_size and
  *               by 0; entries past a request's last page are not read.
  *   max_q_len   a bound of the requests' q_len where cu_q is given, 0 if not
- *               known.  It decides which kernels run, not what they compute.
+ *               known.  It decides which kernels run and how they divide the
+ *               keys, and so the last bits of a result.  A request that is
+ *               longer than it says may be left out (out and lse unwritten).
  *   window      0 for none.
  *   scale       finite.
  *   cu_q        device int32 [n_seq + 1], ascending from 0 to n_tok.  Values
