@@ -38,6 +38,7 @@ struct AttentionArgs {
     uint32_t n_split;
     uint32_t n_work;         // paged_rows.hip: workgroups that share the keys evenly; 0: a workgroup takes a tile
     uint32_t min_rows, max_rows;  // requests of this launch: min_rows <= rows <= max_rows
+    uint32_t of_tile;        // paged_tile.hip: rows of a tile, kFullTile or kHalfTile
     uint32_t tiles_per;      // tiles set aside for each request; 0: as the lengths need (find_tile)
     float scale_log2;        // scale * log2(e)
 };
@@ -138,7 +139,7 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& A, const Request& r
 }
 
 constexpr uint32_t kRowsTile = 16;   // rows of a tile in paged_rows.hip
-constexpr uint32_t tile_rows(uint32_t dim) { return dim == 256 ? 128u : 256u; }  // and in paged_tile.hip
+constexpr uint32_t kFullTile = 256, kHalfTile = 128;  // and in paged_tile.hip; a full one for head_dim 128 only
 constexpr int32_t kRowsBlock = 128;  // keys that a workgroup of paged_rows.hip takes at a time
 constexpr int32_t kTileAlign = 64;   // a split's keys begin at a multiple of this many in paged_tile.hip
 

@@ -14,17 +14,17 @@ namespace {
 
 constexpr uint32_t kWaves = 4;
 
-template <class T, int D>
+template <class T, int D, uint32_t kRows>
 __global__ __launch_bounds__(kWaves * 64) void paged_join_kernel(const AttentionArgs A) {
     constexpr int E = D / 64;  // channels of a lane
     const uint32_t heads = A.cache.n_kv_heads;
     const uint32_t tile_at = blockIdx.x / heads, h = blockIdx.x - tile_at * heads;
-    const Tile tile = find_tile<tile_rows(D)>(A, tile_at);
+    const Tile tile = find_tile<kRows>(A, tile_at);
     if (!tile.live) return;
     const Request req = request_of(A, tile.b);
     const uint32_t rows = req.q_len * A.group;
     if (tile.row0 >= rows || rows < A.min_rows || rows > A.max_rows) return;
-    const uint32_t n_rows = min(tile_rows(D), rows - tile.row0);
+    const uint32_t n_rows = min(kRows, rows - tile.row0);
     const Span span = span_of(A, req, tile.row0, n_rows);
     const int32_t base0 = span.lo & ~(kTileAlign - 1);
     if (span.hi <= base0 || static_cast<uint32_t>(span.hi - base0) <= A.split_tokens) return;  // written whole
@@ -66,21 +66,21 @@ __global__ __launch_bounds__(kWaves * 64) void paged_join_kernel(const Attention
     if (A.lse && lane == 0) A.lse[flat] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
-template <class T, int D>
+template <class T, int D, uint32_t kRows>
 hipError_t join_one(const AttentionArgs& a, hipStream_t stream) {
-    uint32_t most = tile_rows(D);  // rows of a tile
+    uint32_t most = kRows;  // rows of a tile
     if (!a.cu_q) most = std::min(most, a.uniform_q * a.group);
-    const dim3 grid(tile_count<tile_rows(D)>(a) * a.cache.n_kv_heads, (most + kWaves - 1u) / kWaves);
-    hipLaunchKernelGGL((paged_join_kernel<T, D>), grid, dim3(kWaves * 64), 0, stream, a);
+    const dim3 grid(tile_count<kRows>(a) * a.cache.n_kv_heads, (most + kWaves - 1u) / kWaves);
+    hipLaunchKernelGGL((paged_join_kernel<T, D, kRows>), grid, dim3(kWaves * 64), 0, stream, a);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t join_dim(const AttentionArgs& a, uint32_t dim, hipStream_t stream) {
     switch (dim) {
-        case 64: return join_one<T, 64>(a, stream);
-        case 128: return join_one<T, 128>(a, stream);
-        default: return join_one<T, 256>(a, stream);
+        case 64: return join_one<T, 64, kHalfTile>(a, stream);
+        case 128: return a.of_tile == kFullTile ? join_one<T, 128, kFullTile>(a, stream) : join_one<T, 128, kHalfTile>(a, stream);
+        default: return join_one<T, 256, kHalfTile>(a, stream);
     }
 }
 

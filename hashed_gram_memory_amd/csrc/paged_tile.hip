@@ -8,10 +8,10 @@
 // at a row's first keys and hardly ever later.  The work is the two products:
 // bound by the matrix pipes, and next to them by the exponentials.
 //
-// Mapping (gfx950, wave64): a workgroup takes 256 rows of one KV head (head_dim
-// 256: 128 rows) and one split of their keys; each wave holds 32 rows' q,
-// scores and sums in registers.  K and V go through LDS, a tile of KT keys at a
-// time, in rings of four and five buffers.
+// Mapping (gfx950, wave64): a workgroup takes a tile of 256 or 128 rows of one KV
+// head and one split of their keys; each wave holds 32 rows' q, scores and sums
+// in registers.  K and V go through LDS, a tile of KT keys at a time, in rings
+// of four and five buffers.
 //   * S^T = K Q^T on 32x32x16 MFMA: a lane holds a row and 16 of 32 keys, so
 //     the maximum and sum of a row need one exchange between a wave's halves,
 //     and the scores are the second product's B operand as they stand: P never
@@ -26,10 +26,16 @@
 //     turns before they are read; e4m3 codes by way of registers, where they
 //     are widened (exactly).  Addresses come from the page table by scalar
 //     loads, a turn early.
-//   * Eight waves are two on each SIMD, in two halves that take turns: one does
-//     the products of a tile while the other does its softmax and asks for
-//     tiles, so that the matrix pipe and the vector pipe of a SIMD both work.
-//     A head_dim of 256 leaves registers for one wave on a SIMD: no turns.
+//   * The eight waves of a full tile are two on each SIMD, in two halves that
+//     take turns: one does the products of a tile while the other does its
+//     softmax and asks for tiles, so that the matrix pipe and the vector pipe of
+//     a SIMD both work.  The four waves of a half tile leave room for another
+//     workgroup on the CU, which the hardware mixes with it as it comes: better
+//     where tiles differ or are not full, and for head_dim 64 (a batch of 24
+//     requests of 1 to 512 tokens with a window, fp16: 66 us against 73; one of
+//     2,048 over 32,768 keys 678 against 663, e4m3 1,001 against 1,109).  A
+//     head_dim of 256 leaves registers for one wave on a SIMD: half tiles, one
+//     to a CU.
 //
 // What it measured, for 2,048 tokens at the end of 32,768 keys, 32 heads over 8
 // of head_dim 128, bf16: 1,314 us with two buffers, staged through registers,
@@ -123,11 +129,11 @@ __device__ __forceinline__ u32x4v widen(u32x2v w) {
 }
 
 template <class T, int D, bool kE4m3, int kWaves>
-__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(kWaves / 4, kWaves / 4))) void paged_tile_kernel(
+__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2, D == 256 ? 1 : 2))) void paged_tile_kernel(
     const AttentionArgs A) {
     constexpr uint32_t kRows = kWaves * 32u, kThreads = kWaves * 64u;
-    constexpr bool kTurns = kWaves == 8;            // two waves on a SIMD
-    constexpr int KT = D == 256 ? 32 : 64;          // keys of a tile
+    constexpr bool kTurns = kWaves == 8;            // two waves of a workgroup on a SIMD
+    constexpr int KT = kTurns || D == 64 ? 64 : 32; // keys of a tile
     constexpr int TB = KT / 32;                     // blocks of 32 keys
     constexpr int CB = D / 8;                       // 16-byte blocks of a row
     constexpr int CH = D / 16;                      // MFMA steps of a score
@@ -613,10 +619,10 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(kWa
     if (A.lse && g == 0) A.lse[flat] = l == 0.0f ? -INFINITY : (__log2f(l) - nb) * 0.69314718055994531f;
 }
 
-template <class T, int D, bool kE4m3>
+template <class T, int D, bool kE4m3, uint32_t kRows>
 hipError_t tile_one(const AttentionArgs& a, hipStream_t stream) {
-    constexpr int kWaves = tile_rows(D) / 32;
-    const dim3 grid(tile_count<tile_rows(D)>(a) * a.cache.n_kv_heads, a.n_split);
+    constexpr int kWaves = kRows / 32;
+    const dim3 grid(tile_count<kRows>(a) * a.cache.n_kv_heads, a.n_split);
     hipLaunchKernelGGL((paged_tile_kernel<T, D, kE4m3, kWaves>), grid, dim3(kWaves * 64), 0, stream, a);
     return hipGetLastError();
 }
@@ -624,9 +630,11 @@ hipError_t tile_one(const AttentionArgs& a, hipStream_t stream) {
 template <class T, bool kE4m3>
 hipError_t tile_dim(const AttentionArgs& a, uint32_t dim, hipStream_t stream) {
     switch (dim) {
-        case 64: return tile_one<T, 64, kE4m3>(a, stream);
-        case 128: return tile_one<T, 128, kE4m3>(a, stream);
-        default: return tile_one<T, 256, kE4m3>(a, stream);
+        case 64: return tile_one<T, 64, kE4m3, kHalfTile>(a, stream);
+        case 128: 
+            return a.of_tile == kFullTile ? tile_one<T, 128, kE4m3, kFullTile>(a, stream)
+                                          : tile_one<T, 128, kE4m3, kHalfTile>(a, stream);
+        default: return tile_one<T, 256, kE4m3, kHalfTile>(a, stream);
     }
 }
 

@@ -60,27 +60,30 @@ int view_of(const engram_kv_cache* c, CacheView* out) {
 // How one launch divides its keys.
 struct Split {
     uint32_t tokens, n;  // keys of a split (0: all), splits
+    double us;           // what it is expected to take
 };
 
-// Many rows (paged_tile.hip).  A workgroup fills a CU, so a launch takes
-// ceil(groups * n / 256) rounds of a split's keys, and joining writes and reads
-// n fp32 rows for each row; of up to 32 splits the one with the least of both.
-// A round took 0.020, 0.032 and 0.036 us a key for head_dim 64, 128 and 256
-// (2,048 tokens over 32,768 keys, bf16).
-Split split_tiles(uint64_t groups, int64_t most_keys, uint64_t rows, uint32_t dim) {
-    const double key_us = dim == 256 ? 0.036 : 0.008 + 1.9e-4 * dim, join_us = rows * dim * 8.0 / 4e6;
-    double best = 0;
-    Split s = {0u, 1u};
+// Many rows (paged_tile.hip).  A CU holds one workgroup of a full tile, two of
+// half tiles (head_dim 256: one), so a launch takes groups * n / at_once rounds
+// of a split's keys (of equal workgroups, one to a CU: the last is a whole one), and joining writes and reads n fp32 rows for each
+// row; of up to 32 splits the one with the least of both.  A round took, for
+// each key, 0.021, 0.036 and 0.036 us in half tiles of head_dim 64, 128 and 256
+// and 0.032 us in full tiles of 128 (2,048 tokens over 32,768 keys, bf16), and
+// about 5 us to begin and end.
+Split split_tiles(double groups, bool equal, int64_t most_keys, uint64_t rows, uint32_t dim, uint32_t of_tile) {
+    const double key_us = of_tile == kFullTile ? 0.032 : dim == 64 ? 0.021 : 0.036, join_us = rows * dim * 8.0 / 4e6;
+    const double at_once = of_tile == kFullTile || dim == 256 ? 256 : 512;
+    Split s = {0u, 1u, 0.0};
     for (uint32_t n = 1; n <= 32; ++n) {
         const int64_t tokens = ((most_keys + n - 1) / n + 63) / 64 * 64;
         if (n > 1 && tokens < 256) break;
-        const double us = (groups * n + 255) / 256 * tokens * key_us + (n > 1 ? 6 + n * join_us : 0);
-        if (n == 1 || us < best) {
-            best = us;
-            s = {n > 1 ? static_cast<uint32_t>(tokens) : 0u, static_cast<uint32_t>((most_keys + tokens - 1) / tokens)};
-        }
+        const double of_all = groups * n / at_once;
+        const double rounds = equal && at_once == 256 ? ceil(of_all) : std::max(of_all, 1.0);
+        const double us = rounds * (tokens * key_us + 5) + (n > 1 ? 6 + n * join_us : 0);
+        if (n == 1 || us < s.us)
+            s = {n > 1 ? static_cast<uint32_t>(tokens) : 0u, static_cast<uint32_t>((most_keys + tokens - 1) / tokens), us};
     }
-    if (s.n <= 1) s = {0u, 1u};
+    if (s.n <= 1) s.tokens = 0, s.n = 1;
     return s;
 }
 
@@ -200,16 +203,31 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     if (out->any_many) {
         AttentionArgs& m = out->many;
         m.min_rows = out->any_few ? kFewRows + 1 : 0;
-        const uint32_t of_tile = tile_rows(d->cache->head_dim);
-        if (!m.cu_q) m.tiles_per = static_cast<uint32_t>((most_rows + of_tile - 1) / of_tile);
-        const uint64_t groups = (of_tile == 128 ? tile_count<128>(m) : tile_count<256>(m)) * heads;
-        if (groups >= uint64_t(1) << 23) return ENGRAM_ERANGE;  // 512 threads each, and a grid has less than 2^32
+        const uint32_t dim = d->cache->head_dim;
         const uint64_t all_rows = uint64_t(m.n_tok) * d->n_q_heads;
-        const Split s = split_tiles(groups, keys_of(of_tile, kTileAlign), all_rows, d->cache->head_dim);
+        const auto divide = [&](uint32_t of_tile) {
+            m.of_tile = of_tile;
+            if (!m.cu_q) m.tiles_per = static_cast<uint32_t>((most_rows + of_tile - 1) / of_tile);
+            const uint64_t groups = (of_tile == kFullTile ? tile_count<kFullTile>(m) : tile_count<kHalfTile>(m)) * heads;
+            if (groups >> 23) return Split{0u, 0u, 0.0};  // 512 threads each, and a grid has less than 2^32
+            // of the tiles that requests begin, half are expected to be there
+            const double likely = double(groups) - (m.tiles_per ? 0.0 : 0.5 * double(m.n_seq * heads));
+            return split_tiles(likely, !m.cu_q || d->window, keys_of(of_tile, kTileAlign), all_rows, dim, of_tile);
+        };
+        // head_dim 128: full tiles share each key among more rows and take turns (2,048 tokens over 32,768 keys 1,060 us
+        // against 1,190 in half tiles); half tiles leave fewer rows empty and CUs idle (8 requests of 17 tokens, 4 heads
+        // to a key, over 8,192 keys 61 us against 79; 16 of up to 512 with a window of 1,024 126 against 147).
+        Split s = divide(kHalfTile);
+        if (dim == 128) {
+            const Split full = divide(kFullTile);
+            if (full.n && (!s.n || full.us <= s.us)) s = full;
+            else s = divide(kHalfTile);
+        }
+        if (!s.n) return ENGRAM_ERANGE;
         m.split_tokens = s.tokens;
         m.n_split = s.n;
         if (s.n > 1) {
-            out->many_o = up256(s.n * all_rows * d->cache->head_dim * 4);
+            out->many_o = up256(s.n * all_rows * dim * 4);
             out->many_ml = up256(s.n * all_rows * 8);
         }
     }

@@ -195,3 +195,38 @@ def test_many_requests_of_both_kinds():
     lens = [int(rng.integers(n, 120)) for n in new]
     s = _paged(11, F16, False, 64, 1, 2, 8, new, lens)
     _compare(s, _attend(s, max_q_len=70))
+
+
+MANY = [
+    # dtype, e4m3, kv heads, group, page, window, requests, new tokens, longest: more tiles of 256 rows than CUs
+    (BF16, False, 8, 4, 16, 0, 40, 9, 150),
+    (F16, False, 8, 4, 8, 40, 36, 33, 100),
+    (BF16, True, 6, 4, 16, 0, 50, 9, 90),
+    (F16, True, 9, 3, 32, 17, 30, 12, 64),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_attention_of_many_short_chunks(case):
+    """Half tiles of head_dim 128; the same requests, the first with infinities and NaN where others end."""
+    dtype, e4m3, H, G, page, window, n, new, longest = case
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(new // 2, longest, n)]
+    s = _paged(n + page, dtype, e4m3, 128, H, G, page, [new] * n, lens, equal=True)
+    _compare(s, _attend(s, window), window)
+    ragged = [int(x) for x in rng.integers(9, new + 1, n)]
+    s = _paged(n + page + 1, dtype, e4m3, 128, H, G, page, ragged, lens)
+    if not e4m3:  # seen by the last token of the first request alone
+        at = lens[0] - 1
+        where = int(s["table"][0, at // page]), 0, at % page
+        s["v"][where][0], s["v"][where][1] = math.inf, math.nan
+    got = _attend(s, window)
+    if not e4m3:
+        last = ragged[0] - 1
+        assert got[0][last, :G, 0].isinf().all() and got[0][last, :G, 1].isnan().all()
+        assert got[0][:last].isfinite().all() and got[0][last, :, 2:].isfinite().all()
+        s["v"][where][:2] = 0.0
+        got[0][last, :G, :2] = 0.0
+        out = so.attention(s["q"], s["k"], s["v"], s["table"], s["kv_len"], s["cu"], 128 ** -0.5, window)[0]
+        got[0][last, :G, :2] = out[last, :G, :2].to(dtype).cuda()
+    _compare(s, got, window)
