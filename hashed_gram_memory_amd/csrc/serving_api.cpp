@@ -188,11 +188,15 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         // head_dim 128: one request of 512 keys 8.2 us against 9.4 divided, of 1,024 12.5 against 9.5; where there are
         // tiles for every CU, 64 requests of 1,024 keys 40.8 against 43.5).  Else 512 workgroups share all keys: two on
         // each CU keep HBM as busy as three or four do (64 requests of up to 8,192 keys 216 us against 224 and 224), and
-        // leave fewer parts to join.
+        // leave fewer parts to join.  Where a few tiles have all the keys, one on each CU leaves half of the parts (one
+        // request of 131,072 keys 99 us against 104, of 32,768 27.6 against 31.3, head_dim 256 98.6 against 106; from 16
+        // requests on two are better, 115 against 108).  A wave of e4m3 rows has half the bytes in flight, and two of its
+        // workgroups are better throughout (52 us against 56), but for head_dim 256 (57 against 48).
         const int64_t keys = keys_of(f.max_rows, 32);
         const int64_t blocks = (keys + kRowsBlock - 1) / kRowsBlock;
         const bool whole = blocks * d->cache->head_dim <= 512 || (groups >= 512 && blocks <= 8) || groups * blocks >> 31;
-        f.n_work = whole ? 0u : static_cast<uint32_t>(std::min<uint64_t>(groups * blocks, 512));
+        const bool two = groups > 64 || (d->cache->type == ENGRAM_E4M3 && d->cache->head_dim < 256);
+        f.n_work = whole ? 0u : static_cast<uint32_t>(std::min<uint64_t>(groups * blocks, two ? 512 : 256));
         if (f.n_work) {
             const size_t rows = size_t(f.n_work) * 2 * std::min(f.max_rows, kRowsTile);
             out->few_o = up256(rows * d->cache->head_dim * 4);
