@@ -45,7 +45,7 @@
 // products and the other half's softmax issues between them.  Of the time,
 // about a sixth is the card's power: zeros for q, K and V run that much faster.
 //
-// P is rounded once to 16 bits (bf16: half a step is 2^-9 of each p; its
+// P is rounded once to the type of q and out (half a step of each p; their
 // average over the keys adds to the output about what the output's own
 // rounding does).  Twice the digits, as in paged_rows.hip, would cost half as
 // many products again, and here the products are what is waited for.
@@ -140,13 +140,16 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     constexpr int FB = D / 32;                      // blocks of 32 channels
     constexpr int NL = KT * CB / int(kThreads);     // blocks of K (and of V) that a thread brings
     static_assert(NL >= 1 && NL * int(kThreads) == KT * CB, "every thread brings the same");
-    using P = std::conditional_t<kE4m3, Bf16, T>;   // P and V's type; e4m3 codes are exact in both types
+    using P = T;                                    // P and V's type; e4m3 codes are exact in both types
     constexpr uint32_t ES = kE4m3 ? 1 : 2;
     constexpr float kSlack = P::kSlack, kShift = P::kShift;
+    // With codes P is p_j times V's scale, which fp16's range does not hold under a reference of the scores alone: there the
+    // reference is that of c s_j + log2(scale), with the logarithm bounded so that the sum of the p_j stays in fp32's range.
+    constexpr bool kScaled = kE4m3 && std::is_same_v<T, F16>;
 
     __shared__ __attribute__((aligned(1024))) uint16_t sm_k[4][KT * D];
     __shared__ __attribute__((aligned(1024))) uint16_t sm_v[5][KT * D];
-    __shared__ __attribute__((aligned(16))) float sm_scale[8][2][kE4m3 ? KT : 4];
+    __shared__ __attribute__((aligned(16))) float sm_scale[8][kScaled ? 3 : 2][kE4m3 ? KT : 4];
 
     const uint32_t heads = A.cache.n_kv_heads;
     const uint32_t tile_at = blockIdx.x / heads, h = blockIdx.x - tile_at * heads;
@@ -306,6 +309,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     };
     const auto put_scale = [&](int32_t t, float x) __attribute__((always_inline)) {
         if (tid < 2u * KT) sm_scale[t & 7][tid / KT][tid % KT] = x;
+        if constexpr (kScaled)
+            if (tid >= KT && tid < 2u * KT) sm_scale[t & 7][2][tid % KT] = fminf(fmaxf(__log2f(fabsf(x)), -60.0f), 60.0f);
     };
 
     bool all_there = true;  // all pages: else every tile is looked at as one that a mask cuts
@@ -395,11 +400,23 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
             }
         }
         float top = -INFINITY;
+        if constexpr (kScaled) {
 #pragma unroll
-        for (int b = 0; b < TB; ++b)
+            for (int b = 0; b < TB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-        top = max32(top) * c;
+                for (int y = 0; y < 4; ++y) {
+                    const f32x4v by = *reinterpret_cast<const f32x4v*>(&sm_scale[t & 7][2][32 * b + 8 * y + 4 * g]);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) top = fmaxf(top, __builtin_fmaf(s[b][4 * y + z], c, by[z]));
+                }
+            top = max32(top);
+        } else {
+#pragma unroll
+            for (int b = 0; b < TB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+            top = max32(top) * c;
+        }
         if (__any(top > m + kSlack)) {
             const float m_new = fmaxf(m, top);
             const float nb_new = m_new == -INFINITY ? 0.0f : kShift - m_new;

@@ -545,8 +545,8 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  * does not see never reaches its result, NaN and infinities included.
  * Products of 16-bit operands with fp32 sums; softmax in fp32.  For the second
  * product a_j is held in about 16 bits where a request has at most 32 rows (new
- * tokens * n_q_heads / n_kv_heads), and rounded once to `type` (E4M3 caches:
- * to BF16) where it has more.
+ * tokens * n_q_heads / n_kv_heads), and rounded once to `type` where it has
+ * more.
  *
  *   lse         device fp32 [n_tok][n_q_heads], or NULL.
  *   block_table device int32 [n_seq][table_width], rows table_stride apart.  A

@@ -230,3 +230,28 @@ def test_attention_of_many_short_chunks(case):
         out = so.attention(s["q"], s["k"], s["v"], s["table"], s["kv_len"], s["cu"], 128 ** -0.5, window)[0]
         got[0][last, :G, :2] = out[last, :G, :2].to(dtype).cuda()
     _compare(s, got, window)
+
+
+@pytest.mark.parametrize("case", [(64, 2, 3, 16, 0, [150, 40], [500, 40]), (128, 1, 4, 32, 0, [70, 9], [300, 700]),
+                                  (128, 8, 4, 8, 20, [9] * 40, [64] * 40), (256, 1, 2, 16, 33, [90], [140])], ids=str)
+def test_e4m3_weights_keep_the_digits_of_fp16(case):
+    """An fp16 P over an e4m3 cache, with scales of V that differ by 2^17 from key to key, are zero, or all far from 1."""
+    D, H, G, page, window, new, lens = case
+    for far in (0, -24, 20):
+        s = _paged(D + page + far, F16, True, D, H, G, page, new, lens)
+        g = torch.Generator().manual_seed(D + far)
+        by = torch.randint(-14, 4, s["v_scale"].shape, generator=g).double()
+        s["v_scale"] = (s["v_scale"].double() * torch.exp2(by + far)).float()
+        s["v_scale"][torch.rand(s["v_scale"].shape, generator=g) < 0.05] = 0.0
+        if far > 0:
+            s["v_scale"] = s["v_scale"].clamp(max=100.0)  # fp16's range
+        out, lse, mass, move = so.attention(s["q"], s["k"], s["v"], s["table"], s["kv_len"], s["cu"], D ** -0.5, window,
+                                            s["k_scale"], s["v_scale"])
+        ob, lb = so.attention_bounds(out, lse, mass, move, F16, so.half_step(F16))
+        # the product with the scale is rounded in fp32; P is held with its row's largest at 2^7 or more, so that below
+        # 2^-14 it is off by 2^-32 of that largest at most
+        ob = ob + 4 * so.U32 * mass + max(lens) * 2.0 ** -32 * 448 * float(s["v_scale"][s["v_scale"].isfinite()].max())
+        got = _attend(s, window, max_q_len=max(new))
+        _close(got[0], out, ob, ("out", far))
+        empty = lse == -math.inf
+        _close(torch.where(empty, 0.0, got[1].double().cpu()), torch.where(empty, 0.0, lse), torch.where(empty, 0.0, lb), "lse")
