@@ -74,6 +74,7 @@ Split split_tiles(double groups, bool equal, int64_t most_keys, uint64_t rows, u
     const double key_us = of_tile == kFullTile ? 0.032 : dim == 64 ? 0.021 : 0.036, join_us = rows * dim * 8.0 / 4e6;
     const double at_once = of_tile == kFullTile || dim == 256 ? 256 : 512;
     Split s = {0u, 1u, 0.0};
+    most_keys = std::max<int64_t>(most_keys, 1);  // a table of no pages
     for (uint32_t n = 1; n <= 32; ++n) {
         const int64_t tokens = ((most_keys + n - 1) / n + 63) / 64 * 64;
         if (n > 1 && tokens < 256) break;

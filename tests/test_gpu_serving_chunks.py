@@ -255,3 +255,14 @@ def test_e4m3_weights_keep_the_digits_of_fp16(case):
         _close(got[0], out, ob, ("out", far))
         empty = lse == -math.inf
         _close(torch.where(empty, 0.0, got[1].double().cpu()), torch.where(empty, 0.0, lse), torch.where(empty, 0.0, lb), "lse")
+
+
+@pytest.mark.parametrize("tokens", [1, 50])
+def test_attention_without_keys(tokens):
+    """A table of no pages: zeros, and -infinity for lse."""
+    q = torch.randn((2 * tokens, 8, 128), generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    cache = torch.full((3, 2, 16, 128), math.nan, dtype=BF16, device="cuda")
+    table = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    out, lse = lib().paged_attention(q, cache, cache, table, torch.tensor([5, 0], dtype=torch.int32, device="cuda"),
+                                     return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
