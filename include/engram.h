@@ -454,8 +454,8 @@ typedef struct engram_kv_cache {
  *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
  *     t = positions[tok] * inv_freq[i], i = 0 .. rotary_dim/2 - 1,
  * (a, b) = (i, i + rotary_dim/2), or (2i, 2i + 1) with interleaved = 1;
- * elements from rotary_dim on are not rotated.  fp32 arithmetic (angles in
- * fp64), rounded once to `type`.  An output may be its input (same strides);
+ * elements from rotary_dim on are not rotated.  fp32 arithmetic (angles,
+ * cosines and sines in fp64, these rounded to fp32), rounded once to `type`.  An output may be its input (same strides);
  * otherwise they must not overlap.
  *
  *   head_dim    64, 128 or 256.  rotary_dim: a multiple of 16, at most
@@ -463,7 +463,7 @@ typedef struct engram_kv_cache {
  *   n_q_heads, n_k_heads   0 to 65535; 0 leaves that side out.
  *   q_weight, k_weight     device [head_dim] of `type`, 16-byte aligned, or NULL.
  *   positions   device int32 [n_tok], any value.
- *   inv_freq    device double [rotary_dim / 2].
+ *   inv_freq    device double [rotary_dim / 2]; |t| below 2^50.
  *
  * n_tok == 0 is a no-op.  Errors: EINVAL, ERANGE (n_tok > 2^31 - 1, a head
  * count above 65535), EUNSUPPORTED (type, head_dim).
