@@ -14,12 +14,13 @@ attention_example.py runs them together, next to the lookup.
 
 The operators serve: they have no backward, and refuse tensors that require
 a gradient while gradients are recorded.  They run on the current stream of
-their tensors' device, or on ``stream``.  The calls are marshalled by the
+their tensors' device, or on ``stream``, a stream or handle of that device.  The calls are marshalled by the
 extension _serving.so (csrc/serving_binding.cpp); the ctypes structures below are
 the C ABI's descriptions, for callers that hold plain pointers.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -76,10 +77,18 @@ from . import _serving  # noqa: E402
 _serving.setup(_hg.EngramError, torch._C._cuda_getCurrentRawStream, torch.OutOfMemoryError)
 
 
-def _on(stream):
-    """``stream`` as the current one: outputs come from its pool, so that they are not reused while work is queued."""
+def _on(stream, lead):
+    """``stream`` (a torch.cuda.Stream or a handle; 0: the default one) as the current one of the device of ``lead``, the
+    call's first tensor: outputs come from its pool, so that they are not reused while work is queued."""
+    device = getattr(lead, "device", None)
+    if device is None or device.type != "cuda":
+        return contextlib.nullcontext()  # the call refuses it
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        handle = int(stream)
+        # a pointer of 0 would be taken for none given, and get a new stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is one of {stream.device}, not of {device}")
     return torch.cuda.stream(stream)
 
 
@@ -94,7 +103,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     args = (q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
     if stream is None:
         return _serving.qk_norm_rope(*args)
-    with _on(stream):
+    with _on(stream, k if q is None else q):
         return _serving.qk_norm_rope(*args)
 
 
@@ -107,7 +116,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     args = (k, v, k_cache, v_cache, slots, positions, inv_freq, k_weight, eps, interleaved, k_scale, v_scale)
     if stream is None:
         return _serving.kv_append(*args)
-    with _on(stream):
+    with _on(stream, k):
         return _serving.kv_append(*args)
 
 
@@ -128,7 +137,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             workspace, False)
     if stream is None:
         return _serving.paged_attention(*args)
-    with _on(stream):
+    with _on(stream, q):
         return _serving.paged_attention(*args)
 
 
