@@ -8,6 +8,7 @@
 // has the signatures and their documentation.
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 
@@ -54,6 +55,8 @@ struct Args {
         if (t.device() != device) refuse(std::string(name) + " is on " + t.device().str() + ", not on " + device.str());
         if (t.requires_grad() && c10::GradMode::is_enabled())
             refuse(std::string(name) + " requires a gradient, and the operator has no backward");
+        if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+            refuse(std::string(name) + " has a forward gradient, and the operator has no derivative");
         return t;
     }
     // the tensor that says the call's device and type

@@ -13,7 +13,7 @@ page_size] for K and V.
 attention_example.py runs them together, next to the lookup.
 
 The operators serve: they have no backward, and refuse tensors that require
-a gradient while gradients are recorded.  They run on the current stream of
+a gradient while gradients are recorded, and those with a forward gradient.  They run on the current stream of
 their tensors' device, or on ``stream``, a stream or handle of that device.  The calls are marshalled by the
 extension _serving.so (csrc/serving_binding.cpp); the ctypes structures below are
 the C ABI's descriptions, for callers that hold plain pointers.
