@@ -31,7 +31,7 @@ struct AttentionArgs {
     uint32_t table_width;
     uint32_t n_seq;
     uint32_t n_tok;
-    uint32_t uniform_q;      // tokens of each request where cu_q is nullptr
+    uint32_t uniform_q;      // tokens of each request where cu_q is nullptr; a bound of them if there is only one; else 0
     uint32_t group;          // query heads per KV head
     uint32_t window;
     uint32_t split_tokens;   // paged_tile.hip: keys of a split; 0: one split takes all

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kWaves * 64) void paged_join_kernel(const Attention
 template <class T, int D, uint32_t kRows>
 hipError_t join_one(const AttentionArgs& a, hipStream_t stream) {
     uint32_t most = kRows;  // rows of a tile
-    if (!a.cu_q) most = std::min(most, a.uniform_q * a.group);
+    if (a.uniform_q) most = std::min(most, a.uniform_q * a.group);
     const dim3 grid(tile_count<kRows>(a) * a.cache.n_kv_heads, (most + kWaves - 1u) / kWaves);
     hipLaunchKernelGGL((paged_join_kernel<T, D, kRows>), grid, dim3(kWaves * 64), 0, stream, a);
     return hipGetLastError();

@@ -149,7 +149,8 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     a->table_width = static_cast<uint32_t>(d->table_width);
     a->n_seq = static_cast<uint32_t>(d->n_seq);
     a->n_tok = static_cast<uint32_t>(d->n_tok);
-    a->uniform_q = d->cu_q ? 0u : static_cast<uint32_t>(d->n_tok / d->n_seq);
+    const bool alike = !d->cu_q || d->n_seq == 1;  // requests that the host knows the bound of: equal ones, or the only one
+    a->uniform_q = alike ? static_cast<uint32_t>(d->n_tok / d->n_seq) : 0u;
     a->group = d->n_q_heads / view.n_kv_heads;
     a->window = static_cast<uint32_t>(d->window);
     a->scale_log2 = d->scale * 1.4426950408889634f;
@@ -160,17 +161,13 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     a->n_split = 1;
     a->n_work = 0;
     a->part_job = nullptr;
-    if (d->n_seq == 1 && d->cu_q) {  // it can only be the one request
-        a->cu_q = nullptr;
-        a->uniform_q = a->n_tok;
-    }
     const uint64_t heads = view.n_kv_heads, group = a->group;
-    const uint64_t bound = !a->cu_q ? a->uniform_q
-                                    : (d->max_q_len ? std::min<uint64_t>(d->max_q_len, a->n_tok) : a->n_tok);
+    const uint64_t bound = alike ? a->uniform_q
+                                 : (d->max_q_len ? std::min<uint64_t>(d->max_q_len, a->n_tok) : a->n_tok);
     const uint64_t most_rows = bound * group;
     const int64_t all_keys = std::min<int64_t>(d->table_width << view.page_shift, INT32_MAX - 255);
     out->many = *a;
-    out->any_few = a->cu_q || most_rows <= kFewRows;
+    out->any_few = !alike || most_rows <= kFewRows;
     out->any_many = most_rows > kFewRows;
     out->few_o = out->few_ml = out->few_job = out->many_o = out->many_ml = 0;
     // a window bounds the keys of a tile: its own, those of its other tokens, and the step it begins in
@@ -182,7 +179,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         f.max_rows = static_cast<uint32_t>(std::min<uint64_t>(most_rows, kFewRows));
         f.tiles_per = (f.max_rows + kRowsTile - 1) / kRowsTile;
         // without a bound the tiles as the lengths need them may be fewer
-        if (f.cu_q && uint64_t(f.n_tok) * group / kRowsTile + f.n_seq < uint64_t(f.tiles_per) * f.n_seq) f.tiles_per = 0;
+        if (!alike && uint64_t(f.n_tok) * group / kRowsTile + f.n_seq < uint64_t(f.tiles_per) * f.n_seq) f.tiles_per = 0;
         const uint64_t groups = tile_count<kRowsTile>(f) * heads;
         if (groups > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
         // Few keys: a workgroup takes a tile by itself, without the second launch that joins the parts (bf16, 8 KV heads,
@@ -212,12 +209,12 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         const uint64_t all_rows = uint64_t(m.n_tok) * d->n_q_heads;
         const auto divide = [&](uint32_t of_tile) {
             m.of_tile = of_tile;
-            if (!m.cu_q) m.tiles_per = static_cast<uint32_t>((most_rows + of_tile - 1) / of_tile);
+            if (alike) m.tiles_per = static_cast<uint32_t>((most_rows + of_tile - 1) / of_tile);
             const uint64_t groups = (of_tile == kFullTile ? tile_count<kFullTile>(m) : tile_count<kHalfTile>(m)) * heads;
             if (groups >> 23) return Split{0u, 0u, 0.0};  // 512 threads each, and a grid has less than 2^32
             // of the tiles that requests begin, half are expected to be there
             const double likely = double(groups) - (m.tiles_per ? 0.0 : 0.5 * double(m.n_seq * heads));
-            return split_tiles(likely, !m.cu_q || d->window, keys_of(of_tile, kTileAlign), all_rows, dim, of_tile);
+            return split_tiles(likely, alike || d->window, keys_of(of_tile, kTileAlign), all_rows, dim, of_tile);
         };
         // head_dim 128: full tiles share each key among more rows and take turns (2,048 tokens over 32,768 keys 1,060 us
         // against 1,190 in half tiles); half tiles leave fewer rows empty and CUs idle (8 requests of 17 tokens, 4 heads

@@ -128,7 +128,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Causal attention of new tokens ``q`` [n_tok, n_q_heads, head_dim] over a paged cache that holds them: ``out`` of
     q's shape, with ``return_lse`` (out, lse float32 [n_tok, n_q_heads]) (engram_paged_attention).
 
-    Request b has tokens cu_q[b] .. cu_q[b+1]-1 (int32 [n_seq + 1]; None: equally many each) and kv_len[b] cached keys
+    Request b has tokens cu_q[b] .. cu_q[b+1]-1 (int32 [n_seq + 1]; None: equally many each; tokens from cu_q[n_seq] on
+    are no request's, and their rows of the outputs are not written) and kv_len[b] cached keys
     (int32 [n_seq]) on the pages block_table[b] (int32 [n_seq, width]).  ``max_q_len`` bounds the tokens of a request
     where it is known: a batch of single tokens takes fewer launches with it, and a request that is longer may be left
     out.  ``scale`` defaults to head_dim ** -0.5; ``window`` > 0 lets a token see that many keys.

@@ -559,9 +559,10 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  *               longer than it says may be left out (out and lse unwritten).
  *   window      0 for none.
  *   scale       finite.
- *   cu_q        device int32 [n_seq + 1], ascending from 0 to n_tok.  Values
- *               that are not leave results unspecified; nothing out of bounds
- *               is read or written.
+ *   cu_q        device int32 [n_seq + 1], ascending from 0 to n_tok at most:
+ *               tokens from cu_q[n_seq] on are no request's, and their out
+ *               and lse are not written.  Other values leave results
+ *               unspecified; nothing out of bounds is read or written.
  *   ws          device workspace of engram_paged_attention_workspace bytes
  *               (host-only; 0 for few keys), 256-byte aligned.  It holds
  *               nothing between calls; one call at a time may use it.
