@@ -291,7 +291,7 @@ int engram_kv_append(const engram_append_desc* d, void* stream) {
     if (st != ENGRAM_OK) return st;
     if (!good_type(d->type)) return ENGRAM_EUNSUPPORTED;
     if (d->cache->type != ENGRAM_E4M3 && d->cache->type != d->type) return ENGRAM_EUNSUPPORTED;
-    if (d->n_tok < 0 || d->reserved0 != 0) return ENGRAM_EINVAL;
+    if (d->n_tok < 0 || d->reserved0 != 0 || d->reserved1 != 0) return ENGRAM_EINVAL;
     if (d->n_tok > kMaxTokens) return ENGRAM_ERANGE;
     st = check_rotation(d->rotary_dim, d->cache->head_dim, d->n_tok, d->positions, d->inv_freq, d->interleaved, d->eps);
     if (st != ENGRAM_OK) return st;
