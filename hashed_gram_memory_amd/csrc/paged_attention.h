@@ -49,6 +49,9 @@ __device__ __forceinline__ int32_t load_scalar(const int32_t* p) {
     return *(const __attribute__((address_space(4))) int32_t*)(p);
 }
 
+// Keys of a request at most: the kernels ask for a few tiles past a request's last key, whose places are int32 too.
+constexpr int32_t kMostKeys = INT32_MAX - 4095;
+
 // One request as a launch sees it.  Lengths are bounded by what exists, so
 // that no value of cu_q or kv_len leads outside of the buffers.
 struct Request {
@@ -69,7 +72,7 @@ __device__ __forceinline__ Request request_of(const AttentionArgs& A, uint32_t b
         r.q_len = A.uniform_q;
     }
     const uint64_t room = static_cast<uint64_t>(A.table_width) << A.cache.page_shift;
-    const int32_t most = room < 0x7FFFFF00ull ? static_cast<int32_t>(room) : 0x7FFFFF00;
+    const int32_t most = room < static_cast<uint64_t>(kMostKeys) ? static_cast<int32_t>(room) : kMostKeys;
     r.kv_len = min(max(A.kv_len[b], 0), most);
     return r;
 }

@@ -165,7 +165,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     const uint64_t bound = alike ? a->uniform_q
                                  : (d->max_q_len ? std::min<uint64_t>(d->max_q_len, a->n_tok) : a->n_tok);
     const uint64_t most_rows = bound * group;
-    const int64_t all_keys = std::min<int64_t>(d->table_width << view.page_shift, INT32_MAX - 255);
+    const int64_t all_keys = std::min<int64_t>(d->table_width << view.page_shift, kMostKeys);
     out->many = *a;
     out->any_few = !alike || most_rows <= kFewRows;
     out->any_many = most_rows > kFewRows;

@@ -551,8 +551,8 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  *   lse         device fp32 [n_tok][n_q_heads], or NULL.
  *   block_table device int32 [n_seq][table_width], rows table_stride apart.  A
  *               page number outside the pool is never read: its keys count
- *               as unseen.  kv_len is bounded by table_width * page_size and
- *               by 0; entries past a request's last page are not read.
+ *               as unseen.  kv_len is bounded by table_width * page_size, by
+ *               2^31 - 4096 and by 0; entries past a request's last page are not read.
  *   max_q_len   a bound of the requests' q_len where cu_q is given, 0 if not
  *               known.  It decides which kernels run and how they divide the
  *               keys, and so the last bits of a result.  A request that is
