@@ -16,6 +16,7 @@ Functions mirror the C ABI in include/engram.h:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from dataclasses import dataclass
 
@@ -562,4 +563,20 @@ def probe_rows(plan: Plan, addr: torch.Tensor, out: torch.Tensor, stream=None) -
     return out
 
 
-from .serving import kv_append, paged_attention, paged_attention_workspace, qk_norm_rope  # noqa: E402  (the binding above comes first)
+# The serving operators (serving.py) are loaded when the first of them is named: their extension belongs to one build of
+# torch, and the lookup does without it.
+_SERVING = ("kv_append", "paged_attention", "paged_attention_workspace", "qk_norm_rope")
+
+
+def __getattr__(name: str):
+    if name != "serving" and name not in _SERVING:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    module = importlib.import_module(".serving", __name__)
+    if name == "serving":
+        return module
+    globals().update({n: getattr(module, n) for n in _SERVING})
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), "serving", *_SERVING})
