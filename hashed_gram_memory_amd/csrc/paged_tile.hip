@@ -107,13 +107,12 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
         reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)(p)));
 }
 // 16 bytes of each lane to LDS, lane after lane from an address that is the same for all.  The compiler knows of no such
-// load: wait_loads is to stand between it and the barrier that its readers wait for.  M0 holds the LDS address; nothing
-// else in this kernel uses it.
+// load: wait_loads is to stand between it and the barrier that its readers wait for.  M0 holds the LDS address.
 __device__ __forceinline__ void to_lds(uint64_t base, uint32_t offset, uint32_t to) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
                  : "v"(offset), "s"(base), "s"(to)
-                 : "memory");
+                 : "m0", "memory");
 }
 // all but the last kMost loads have come
 template <int kMost>
