@@ -34,8 +34,8 @@ struct AttentionArgs {
     uint32_t uniform_q;      // tokens of each request where cu_q is nullptr; a bound of them if there is only one; else 0
     uint32_t group;          // query heads per KV head
     uint32_t window;
-    uint32_t split_tokens;   // paged_tile.hip: keys of a split; 0: one split takes all
-    uint32_t n_split;
+    uint32_t split_tokens;   // paged_tile.hip: keys of a split at most (split_keys); 0: one split takes all
+    uint32_t n_split;        // splits of a tile at most
     uint32_t n_work;         // paged_rows.hip: workgroups that share the keys evenly; 0: a workgroup takes a tile
     uint32_t min_rows, max_rows;  // requests of this launch: min_rows <= rows <= max_rows
     uint32_t of_tile;        // paged_tile.hip: rows of a tile, kFullTile or kHalfTile
@@ -139,6 +139,29 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& A, const Request& r
     s.hi = last + 1;
     s.lo = A.window && first >= static_cast<int32_t>(A.window) ? first - static_cast<int32_t>(A.window) + 1 : 0;
     return s;
+}
+
+constexpr uint32_t kLeastSplit = 256;  // keys of a split in paged_tile.hip at least
+
+// Keys of a split in a divided launch of paged_tile.hip: of the longest of its requests, which the host does not know,
+// n_split at most.  The host bounds them by the table's width, and a table is often as wide as the longest context that a
+// server allows: 64 tokens over 4,096 keys (32 heads over 8 of 128, bf16) with a table for 131,072 took 127 us by that bound
+// alone and take 27.2 now; with a table for 4,096 they took 26.9.  Looking at the lengths of several requests costs 1 us (24
+// requests of up to 64 tokens over up to 8,192 keys 212.5 us against 211).  The same for all waves of the launch and the join.
+__device__ __forceinline__ uint32_t split_keys(const AttentionArgs& A, const Request& req) {
+    if (A.split_tokens == 0u) return 0u;
+    int32_t longest = req.kv_len;
+    if (A.n_seq > 1u) {
+        for (uint32_t b = threadIdx.x & 63u; b < A.n_seq; b += 64u) {
+            const Request r = request_of(A, b);
+            const uint32_t rows = r.q_len * A.group;
+            if (rows >= max(A.min_rows, 1u) && rows <= A.max_rows) longest = max(longest, r.kv_len);
+        }
+        for (uint32_t k = 1; k < min(A.n_seq, 64u); k <<= 1) longest = max(longest, __shfl_xor(longest, static_cast<int>(k)));
+    }
+    const uint32_t keys = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(longest));
+    const uint32_t even = ((keys + A.n_split - 1u) / A.n_split + 63u) & ~63u;
+    return min(A.split_tokens, max(even, kLeastSplit));
 }
 
 constexpr uint32_t kRowsTile = 16;   // rows of a tile in paged_rows.hip

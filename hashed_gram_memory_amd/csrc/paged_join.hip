@@ -27,8 +27,9 @@ __global__ __launch_bounds__(kWaves * 64) void paged_join_kernel(const Attention
     const uint32_t n_rows = min(kRows, rows - tile.row0);
     const Span span = span_of(A, req, tile.row0, n_rows);
     const int32_t base0 = span.lo & ~(kTileAlign - 1);
-    if (span.hi <= base0 || static_cast<uint32_t>(span.hi - base0) <= A.split_tokens) return;  // written whole
-    const uint32_t n_split = (static_cast<uint32_t>(span.hi - base0) + A.split_tokens - 1u) / A.split_tokens;
+    const uint32_t of_split = split_keys(A, req);
+    if (span.hi <= base0 || static_cast<uint32_t>(span.hi - base0) <= of_split) return;  // written whole
+    const uint32_t n_split = (static_cast<uint32_t>(span.hi - base0) + of_split - 1u) / of_split;
 
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
     const uint32_t of_tile = blockIdx.y * kWaves + wave;

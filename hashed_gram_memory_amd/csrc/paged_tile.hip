@@ -165,13 +165,14 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     // this split's keys [c0, c1)
     const int32_t base0 = span.lo & ~(kTileAlign - 1);
     const uint32_t split = blockIdx.y;
-    const bool divided = A.split_tokens != 0 && span.hi > base0 && static_cast<uint32_t>(span.hi - base0) > A.split_tokens;
+    const uint32_t of_split = split_keys(A, req);
+    const bool divided = of_split != 0 && span.hi > base0 && static_cast<uint32_t>(span.hi - base0) > of_split;
     int32_t c0 = base0, c1 = max(span.hi, base0);
     if (divided) {
-        const int64_t at = static_cast<int64_t>(base0) + static_cast<int64_t>(split) * A.split_tokens;
+        const int64_t at = static_cast<int64_t>(base0) + static_cast<int64_t>(split) * of_split;
         if (at >= span.hi) return;
         c0 = static_cast<int32_t>(at);
-        c1 = static_cast<int32_t>(min(at + A.split_tokens, static_cast<int64_t>(span.hi)));
+        c1 = static_cast<int32_t>(min(at + of_split, static_cast<int64_t>(span.hi)));
     } else if (split != 0) {
         return;
     }

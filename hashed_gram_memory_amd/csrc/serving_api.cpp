@@ -59,7 +59,7 @@ int view_of(const engram_kv_cache* c, CacheView* out) {
 
 // How one launch divides its keys.
 struct Split {
-    uint32_t tokens, n;  // keys of a split (0: all), splits
+    uint32_t tokens, n;  // keys of a split (0: all), splits; at most
     double us;           // what it is expected to take
 };
 
@@ -77,7 +77,7 @@ Split split_tiles(double groups, bool equal, int64_t most_keys, uint64_t rows, u
     most_keys = std::max<int64_t>(most_keys, 1);  // a table of no pages
     for (uint32_t n = 1; n <= 32; ++n) {
         const int64_t tokens = ((most_keys + n - 1) / n + 63) / 64 * 64;
-        if (n > 1 && tokens < 256) break;
+        if (n > 1 && tokens < kLeastSplit) break;
         const double of_all = groups * n / at_once;
         const double rounds = equal && at_once == 256 ? ceil(of_all) : std::max(of_all, 1.0);
         const double us = rounds * (tokens * key_us + 5) + (n > 1 ? 6 + n * join_us : 0);

@@ -554,8 +554,8 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  *               as unseen.  kv_len is bounded by table_width * page_size, by
  *               2^31 - 4096 and by 0; entries past a request's last page are not read.
  *   max_q_len   a bound of the requests' q_len where cu_q is given, 0 if not
- *               known.  It decides which kernels run and how they divide the
- *               keys, and so the last bits of a result.  A request that is
+ *               known.  It and the requests' lengths decide which kernels run
+ *               and how they divide the keys, and so the last bits of a result.  A request that is
  *               longer than it says may be left out (out and lse unwritten).
  *   window      0 for none.
  *   scale       finite.
