@@ -211,11 +211,14 @@ __device__ __forceinline__ Divisor divisor_of(float amax) {
     return v;
 }
 
-// Eight e4m3 codes of x * 448 / amax, nearest even.  x * 448 is exact for
-// 16-bit inputs (448 = 7 * 2^6); a product with the reciprocal, put right by
-// its remainder (exact in one fused step), is the quotient wherever that is an
-// fp32 number, so that one half-way between two codes is seen as such.  A
-// third of the instructions of 8 divisions.
+// Eight e4m3 codes of x * 448 / amax, nearest even.  x * 448 is exact where x
+// is a 16-bit number (448 = 7 * 2^6): values, and what of a key is neither
+// normed nor turned.  For other keys, fp32 numbers, it is one fp32 rounding
+// more, which moves a code in 10^6 next to a tie, as those before it do.  A
+// product with the reciprocal, put right by its remainder (exact in one fused
+// step), is the quotient wherever that is an fp32 number, so that one half-way
+// between two codes is seen as such.  A third of the instructions of 8
+// divisions.
 __device__ __forceinline__ u32x2v encode8(const float* x, const Divisor& v) {
     float q[8];
 #pragma unroll

@@ -4,9 +4,12 @@
 //     s_j = scale * log2(e) * (q . k_j)
 //
 // One pass over the keys with a running maximum and sum.  The work is the
-// reading of K and V, each byte once per KV head: HBM-bound.  64 requests of
-// 8,192 keys (8 KV heads, head_dim 128, bf16) take 360 us, 6.0 TB/s, where a
-// streaming read reaches 6.7 to 6.9; over e4m3 192 us, 5.8 TB/s.
+// reading of K and V, each byte once for every 16 rows of its KV head (once for
+// a single token of up to 16 heads to a key, twice for 17 to 32 rows):
+// HBM-bound.  64 requests of up to 8,192 keys (8 KV heads, head_dim 128, bf16)
+// take 218 us, 5.6 TB/s, where a streaming read reaches 6.7 to 6.9, and over
+// e4m3 131 us, 4.8 TB/s; with all of them full 360 us, 6.0 TB/s, and 192 us,
+// 5.8 TB/s.
 //
 // Mapping (gfx950, wave64): a workgroup takes one tile of 16 rows of one KV
 // head and a run of its keys; its 4 waves take 32 keys each in turn, straight

@@ -31,11 +31,13 @@
 //     softmax and asks for tiles, so that the matrix pipe and the vector pipe of
 //     a SIMD both work.  The four waves of a half tile leave room for another
 //     workgroup on the CU, which the hardware mixes with it as it comes: better
-//     where tiles differ or are not full, and for head_dim 64 (a batch of 24
-//     requests of 1 to 512 tokens with a window, fp16: 66 us against 73; one of
-//     2,048 over 32,768 keys 678 against 663, e4m3 1,001 against 1,109).  A
-//     head_dim of 256 leaves registers for one wave on a SIMD: half tiles, one
-//     to a CU.
+//     where tiles differ or are not full.  For head_dim 64 all tiles are half
+//     ones: a batch of 24 requests of 1 to 512 tokens with a window, fp16, took
+//     66 us against 73 and a chunk of 2,048 over 32,768 keys of e4m3 1,001
+//     against 1,109, for which the same chunk over 16 bits is 2% slower (678
+//     against 663).  A head_dim of 256 leaves registers for one wave on a SIMD:
+//     half tiles, one to a CU.  Over e4m3, whose tiles pass through registers,
+//     full tiles spill 6 registers and head_dim 256 some 65.
 //
 // What it measured, for 2,048 tokens at the end of 32,768 keys, 32 heads over 8
 // of head_dim 128, bf16: 1,314 us with two buffers, staged through registers,
@@ -47,8 +49,11 @@
 //
 // P is rounded once to the type of q and out (half a step of each p; their
 // average over the keys adds to the output about what the output's own
-// rounding does).  Twice the digits, as in paged_rows.hip, would cost half as
-// many products again, and here the products are what is waited for.
+// rounding does: 2.4e-3 of it in bf16 where 1.7e-3 are the output's, 2.9e-4 and
+// 2.1e-4 in fp16).  Twice the digits, as in paged_rows.hip, are half as many
+// products again, and here the products are what is waited for: with them the
+// chunk took 1,450 us for 1,097, the batch of 24 requests 72.0 for 62.7, the
+// chunk of head_dim 64 893 for 699.
 //
 // What a row does not see: scores of hidden keys become -inf before the
 // maximum, and their p is 0.  A key that no row sees (past the end, before the

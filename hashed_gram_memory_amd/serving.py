@@ -132,7 +132,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     are no request's, and their rows of the outputs are not written) and kv_len[b] cached keys
     (int32 [n_seq]) on the pages block_table[b] (int32 [n_seq, width]).  ``max_q_len`` bounds the tokens of a request
     where it is known: a batch of single tokens takes fewer launches with it, and a request that is longer may be left
-    out.  ``scale`` defaults to head_dim ** -0.5; ``window`` > 0 lets a token see that many keys.
+    out.  Softmax weights are held in about 16 bits where a request has at most 32 rows (tokens * query heads of a key)
+    and are rounded once to q's type where it has more, which adds to the output about what its own rounding does.  ``scale`` defaults to head_dim ** -0.5; ``window`` > 0 lets a token see that many keys.
     ``workspace``: uint8 of paged_attention_workspace bytes, 256-byte aligned; allocated if not given."""
     args = (q, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, scale, window, k_scale, v_scale, out, return_lse,
             workspace, False)

@@ -555,8 +555,9 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  *               2^31 - 4096 and by 0; entries past a request's last page are not read.
  *   max_q_len   a bound of the requests' q_len where cu_q is given, 0 if not
  *               known.  It and the requests' lengths decide which kernels run
- *               and how they divide the keys, and so the last bits of a result.  A request that is
- *               longer than it says may be left out (out and lse unwritten).
+ *               and how they divide the keys, and so the last bits of a
+ *               result.  A request that is longer than it says may be left out
+ *               (out and lse unwritten).
  *   window      0 for none.
  *   scale       finite.
  *   cu_q        device int32 [n_seq + 1], ascending from 0 to n_tok at most:
