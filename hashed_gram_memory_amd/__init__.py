@@ -565,7 +565,8 @@ def probe_rows(plan: Plan, addr: torch.Tensor, out: torch.Tensor, stream=None) -
 
 # The serving operators (serving.py) are loaded when the first of them is named: their extension belongs to one build of
 # torch, and the lookup does without it.
-_SERVING = ("kv_append", "paged_attention", "paged_attention_workspace", "qk_norm_rope")
+_SERVING = ("kv_append", "kv_append_pages", "page_tables", "page_tables_workspace", "paged_attention",
+            "paged_attention_workspace", "qk_norm_rope", "verify_draft", "verify_draft_workspace")
 
 
 def __getattr__(name: str):

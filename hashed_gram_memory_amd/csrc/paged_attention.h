@@ -49,6 +49,10 @@ __device__ __forceinline__ int32_t load_scalar(const int32_t* p) {
     return *(const __attribute__((address_space(4))) int32_t*)(p);
 }
 
+__device__ __forceinline__ float load_scalar(const float* p) {
+    return *(const __attribute__((address_space(4))) float*)(p);
+}
+
 // Keys of a request at most: the kernels ask for a few tiles past a request's last key, whose places are int32 too.
 constexpr int32_t kMostKeys = INT32_MAX - 4095;
 
@@ -169,8 +173,8 @@ constexpr uint32_t kFullTile = 256, kHalfTile = 128;  // and in paged_tile.hip; 
 constexpr int32_t kRowsBlock = 128;  // keys that a workgroup of paged_rows.hip takes at a time
 constexpr int32_t kTileAlign = 64;   // a split's keys begin at a multiple of this many in paged_tile.hip
 
-hipError_t launch_paged_rows(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
-hipError_t launch_paged_tile(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
+hipError_t launch_paged_rows(const AttentionArgs& a, uint32_t dim, uint32_t type, Held held, hipStream_t stream);
+hipError_t launch_paged_tile(const AttentionArgs& a, uint32_t dim, uint32_t type, Held held, hipStream_t stream);
 // Joins the parts of a divided launch of launch_paged_tile (launch_paged_rows joins its own).
 hipError_t launch_paged_join(const AttentionArgs& a, uint32_t dim, uint32_t type, hipStream_t stream);
 

@@ -190,14 +190,16 @@ __device__ __forceinline__ Share share_of(const AttentionArgs& A, ShareLds& sm) 
     return s;
 }
 
-template <class T, int D, bool kE4m3>
+template <class T, int D, int kHeld>
 __global__ __launch_bounds__(kWaves * 64)
     __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : D == 64 ? 3 : 2))) void paged_rows_kernel(const AttentionArgs args) {
+    constexpr bool kE4m3 = kHeld != kHalves;  // codes, of either kind
+    constexpr bool kPages = kHeld == kE4m3Pages || kHeld == kI8Pages;  // one scale for a page and head
     constexpr int EPL = D / 16;              // channels of V in a lane
     constexpr uint32_t CH = D / 32;          // MFMA steps of a score
     constexpr int ES = kE4m3 ? 1 : 2;        // bytes of an element
     constexpr int OP = D + 4;                // padded row of partial sums
-    // P and V's type.  An e4m3 V is exact in bf16, whose range holds p * scale.
+    // P and V's type.  A code is exact in bf16, whose range holds p * scale.
     using P = std::conditional_t<kE4m3, Bf16, T>;
     __shared__ ShareLds sm_share;
     __shared__ float sm_o[kWaves * kRows * OP];
@@ -282,6 +284,7 @@ __global__ __launch_bounds__(kWaves * 64)
         Words<16> kw[2][ES == 1 ? CH / 2 : CH];  // keys base + n and base + 16 + n
         Words<EPL * ES> vw[2][4];                // keys base + 4g + 0..3 and base + 16 + 4g + 0..3, which are also this lane's scores
         f32x4v ks[2], vs[2];
+        float kp[4], vp[4];  // scales of the pages of a step's runs of 8 keys
         auto ask_k = [&](int32_t base, const Pages& pg) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -291,7 +294,11 @@ __global__ __launch_bounds__(kWaves * 64)
 #pragma unroll
                 for (uint32_t i = 0; i < (ES == 1 ? CH / 2 : CH); ++i)
                     kw[t][i] = load_words<16>(p + (ES == 1 ? 64 * i + 16 * g : (32 * i + 8 * g) * 2));
-                if constexpr (kE4m3) {
+                if constexpr (kPages) {
+#pragma unroll
+                    for (int i = 2 * t; i < 2 * t + 2; ++i)
+                        kp[i] = load_scalar(A.cache.k_scale + (static_cast<int64_t>(max(pg.p[i], 0)) * heads + h));
+                } else if constexpr (kE4m3) {
                     const int64_t c = max(pg.p[2 * t], 0), d = max(pg.p[2 * t + 1], 0);
                     const uint32_t at = (static_cast<uint32_t>(base) + 16 * t + 4u * g) & in_page;
                     ks[t] = *reinterpret_cast<const f32x4v*>(A.cache.k_scale + ((((g >> 1 ? d : c) * heads) << shift) + of_head + at));
@@ -306,7 +313,11 @@ __global__ __launch_bounds__(kWaves * 64)
                 const uint8_t* p = vh + ((g >> 1 ? b : a) + static_cast<int64_t>(key * D + n * EPL)) * ES;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) vw[t][i] = load_words<EPL * ES>(p + i * D * ES);
-                if constexpr (kE4m3) {
+                if constexpr (kPages) {
+#pragma unroll
+                    for (int i = 2 * t; i < 2 * t + 2; ++i)
+                        vp[i] = load_scalar(A.cache.v_scale + (static_cast<int64_t>(max(pg.p[i], 0)) * heads + h));
+                } else if constexpr (kE4m3) {
                     const int64_t c = max(pg.p[2 * t], 0), d = max(pg.p[2 * t + 1], 0);
                     vs[t] = *reinterpret_cast<const f32x4v*>(A.cache.v_scale + ((((g >> 1 ? d : c) * heads) << shift) + of_head + key));
                 }
@@ -350,8 +361,8 @@ __global__ __launch_bounds__(kWaves * 64)
                         u32x4v a;
                         if constexpr (kE4m3) {
                             const uint32_t w0 = kw[t][c / 2].w[2 * (c % 2)], w1 = kw[t][c / 2].w[2 * (c % 2) + 1];
-                            a = u32x4v{T::template from_e4m3<false>(w0), T::template from_e4m3<true>(w0),
-                                       T::template from_e4m3<false>(w1), T::template from_e4m3<true>(w1)};
+                            a = u32x4v{from_codes<T, kHeld, false>(w0), from_codes<T, kHeld, true>(w0),
+                                       from_codes<T, kHeld, false>(w1), from_codes<T, kHeld, true>(w1)};
                         } else {
                             a = u32x4v{kw[t][c].w[0], kw[t][c].w[1], kw[t][c].w[2], kw[t][c].w[3]};
                         }
@@ -360,12 +371,18 @@ __global__ __launch_bounds__(kWaves * 64)
                 }
                 float x[2][4];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t) {
+                    float by = A.scale_log2;
+                    if constexpr (kPages) {
+                        const float a = kp[2 * t], b = kp[2 * t + 1];
+                        by *= g >> 1 ? b : a;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[t][i] = s[t][i] * A.scale_log2;
-                        if constexpr (kE4m3) x[t][i] *= ks[t][i];
+                        x[t][i] = s[t][i] * by;
+                        if constexpr (kE4m3 && !kPages) x[t][i] *= ks[t][i];
                     }
+                }
                 if (next < c1) ask_k(next, ahead);
 
                 // every row of the tile sees every key of a whole step; else each row's own keys
@@ -402,13 +419,20 @@ __global__ __launch_bounds__(kWaves * 64)
                 }
                 float p[2][4];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t) {
+                    float vs_page = 0.0f;
+                    if constexpr (kPages) {
+                        const float a = vp[2 * t], b = vp[2 * t + 1];
+                        vs_page = g >> 1 ? b : a;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         p[t][i] = __builtin_amdgcn_exp2f(x[t][i] + nb);
                         l += p[t][i];
-                        if constexpr (kE4m3) p[t][i] = (seen >> (16 * t + i)) & 1u ? p[t][i] * vs[t][i] : 0.0f;
+                        if constexpr (kE4m3)
+                            p[t][i] = (seen >> (16 * t + i)) & 1u ? p[t][i] * (kPages ? vs_page : vs[t][i]) : 0.0f;
                     }
+                }
 
                 // V rows as 16-bit pairs of channels
                 typedef Words<EPL * 2> Pairs;
@@ -420,8 +444,8 @@ __global__ __launch_bounds__(kWaves * 64)
                         if constexpr (kE4m3) {
 #pragma unroll
                             for (int e = 0; e < EPL / 2; ++e)
-                                v[4 * t + i].w[e] = (e & 1) ? P::template from_e4m3<true>(vw[t][i].w[e / 2])
-                                                            : P::template from_e4m3<false>(vw[t][i].w[e / 2]);
+                                v[4 * t + i].w[e] = (e & 1) ? from_codes<P, kHeld, true>(vw[t][i].w[e / 2])
+                                                            : from_codes<P, kHeld, false>(vw[t][i].w[e / 2]);
                         } else {
                             v[4 * t + i] = vw[t][i];
                         }
@@ -637,30 +661,39 @@ __global__ __launch_bounds__(256) void rows_join_kernel(const AttentionArgs A) {
             sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
-template <class T, int D, bool kE4m3>
+template <class T, int D, int kHeld>
 hipError_t rows_one(const AttentionArgs& a, hipStream_t stream) {
     const uint32_t groups = a.n_work ? a.n_work : tile_count<kRows>(a) * a.cache.n_kv_heads;
-    hipLaunchKernelGGL((paged_rows_kernel<T, D, kE4m3>), dim3(groups), dim3(kWaves * 64), 0, stream, a);
+    hipLaunchKernelGGL((paged_rows_kernel<T, D, kHeld>), dim3(groups), dim3(kWaves * 64), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.n_work) return e;
     hipLaunchKernelGGL((rows_join_kernel<T, D>), dim3(a.n_work, std::min(a.max_rows, kRows)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
-template <class T, bool kE4m3>
+template <class T, int kHeld>
 hipError_t rows_dim(const AttentionArgs& a, uint32_t dim, hipStream_t stream) {
     switch (dim) {
-        case 64: return rows_one<T, 64, kE4m3>(a, stream);
-        case 128: return rows_one<T, 128, kE4m3>(a, stream);
-        default: return rows_one<T, 256, kE4m3>(a, stream);
+        case 64: return rows_one<T, 64, kHeld>(a, stream);
+        case 128: return rows_one<T, 128, kHeld>(a, stream);
+        default: return rows_one<T, 256, kHeld>(a, stream);
+    }
+}
+
+template <class T>
+hipError_t rows_held(const AttentionArgs& a, uint32_t dim, Held held, hipStream_t stream) {
+    switch (held) {
+        case kHalves: return rows_dim<T, kHalves>(a, dim, stream);
+        case kE4m3Rows: return rows_dim<T, kE4m3Rows>(a, dim, stream);
+        case kE4m3Pages: return rows_dim<T, kE4m3Pages>(a, dim, stream);
+        default: return rows_dim<T, kI8Pages>(a, dim, stream);
     }
 }
 
 }  // namespace
 
-hipError_t launch_paged_rows(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream) {
-    if (type == ENGRAM_BF16) return e4m3 ? rows_dim<Bf16, true>(a, dim, stream) : rows_dim<Bf16, false>(a, dim, stream);
-    return e4m3 ? rows_dim<F16, true>(a, dim, stream) : rows_dim<F16, false>(a, dim, stream);
+hipError_t launch_paged_rows(const AttentionArgs& a, uint32_t dim, uint32_t type, Held held, hipStream_t stream) {
+    return type == ENGRAM_BF16 ? rows_held<Bf16>(a, dim, held, stream) : rows_held<F16>(a, dim, held, stream);
 }
 
 }  // namespace engram

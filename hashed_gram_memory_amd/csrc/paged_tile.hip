@@ -125,16 +125,18 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kMost) : "memory");
 }
 
-// eight e4m3 codes as 16-bit numbers
-template <class T>
+// eight codes as 16-bit numbers
+template <class T, int kHeld>
 __device__ __forceinline__ u32x4v widen(u32x2v w) {
-    return u32x4v{T::template from_e4m3<false>(w[0]), T::template from_e4m3<true>(w[0]), T::template from_e4m3<false>(w[1]),
-                  T::template from_e4m3<true>(w[1])};
+    return u32x4v{from_codes<T, kHeld, false>(w[0]), from_codes<T, kHeld, true>(w[0]), from_codes<T, kHeld, false>(w[1]),
+                  from_codes<T, kHeld, true>(w[1])};
 }
 
-template <class T, int D, bool kE4m3, int kWaves>
+template <class T, int D, int kHeld, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2, D == 256 ? 1 : 2))) void paged_tile_kernel(
     const AttentionArgs A) {
+    constexpr bool kE4m3 = kHeld != kHalves;        // codes, of either kind
+    constexpr bool kPages = kHeld == kE4m3Pages || kHeld == kI8Pages;  // one scale for a page and head
     constexpr uint32_t kRows = kWaves * 32u, kThreads = kWaves * 64u;
     constexpr bool kTurns = kWaves == 8;            // two waves of a workgroup on a SIMD
     constexpr int KT = kTurns || D == 64 ? 64 : 32; // keys of a tile
@@ -144,7 +146,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     constexpr int FB = D / 32;                      // blocks of 32 channels
     constexpr int NL = KT * CB / int(kThreads);     // blocks of K (and of V) that a thread brings
     static_assert(NL >= 1 && NL * int(kThreads) == KT * CB, "every thread brings the same");
-    using P = T;                                    // P and V's type; e4m3 codes are exact in both types
+    using P = T;                                    // P and V's type; codes are exact in both types
     constexpr uint32_t ES = kE4m3 ? 1 : 2;
     constexpr float kSlack = P::kSlack, kShift = P::kShift;
     // With codes P is p_j times V's scale, which fp16's range does not hold under a reference of the scores alone: there the
@@ -297,8 +299,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const uint32_t at = (i * kThreads + tid) * 8u;
-            *reinterpret_cast<u32x4v*>(&sm_k[t & 3][at]) = widen<T>(r.k[i]);
-            *reinterpret_cast<u32x4v*>(&sm_v[static_cast<uint32_t>(t) % 5u][at]) = widen<P>(r.v[i]);
+            *reinterpret_cast<u32x4v*>(&sm_k[t & 3][at]) = widen<T, kHeld>(r.k[i]);
+            *reinterpret_cast<u32x4v*>(&sm_v[static_cast<uint32_t>(t) % 5u][at]) = widen<P, kHeld>(r.v[i]);
         }
     };
     // the scale of key tid % KT: of K (tid < KT), of V
@@ -310,7 +312,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         const uint32_t in = (static_cast<uint32_t>(base_of(t)) + tid % KT) & in_page;
         const float* from = tid < KT ? A.cache.k_scale : A.cache.v_scale;
         const bool ok = page >= 0 && page < A.cache.n_pages;
-        return ok ? from[((static_cast<int64_t>(page) * heads + h) << shift) + in] : 0.0f;
+        const int64_t of_page = static_cast<int64_t>(page) * heads + h;
+        return ok ? from[kPages ? of_page : (of_page << shift) + in] : 0.0f;
     };
     const auto put_scale = [&](int32_t t, float x) __attribute__((always_inline)) {
         if (tid < 2u * KT) sm_scale[t & 7][tid / KT][tid % KT] = x;
@@ -647,30 +650,39 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     if (A.lse && g == 0) A.lse[flat] = l == 0.0f ? -INFINITY : (__log2f(l) - nb) * 0.69314718055994531f;
 }
 
-template <class T, int D, bool kE4m3, uint32_t kRows>
+template <class T, int D, int kHeld, uint32_t kRows>
 hipError_t tile_one(const AttentionArgs& a, hipStream_t stream) {
     constexpr int kWaves = kRows / 32;
     const dim3 grid(tile_count<kRows>(a) * a.cache.n_kv_heads, a.n_split);
-    hipLaunchKernelGGL((paged_tile_kernel<T, D, kE4m3, kWaves>), grid, dim3(kWaves * 64), 0, stream, a);
+    hipLaunchKernelGGL((paged_tile_kernel<T, D, kHeld, kWaves>), grid, dim3(kWaves * 64), 0, stream, a);
     return hipGetLastError();
 }
 
-template <class T, bool kE4m3>
+template <class T, int kHeld>
 hipError_t tile_dim(const AttentionArgs& a, uint32_t dim, hipStream_t stream) {
     switch (dim) {
-        case 64: return tile_one<T, 64, kE4m3, kHalfTile>(a, stream);
+        case 64: return tile_one<T, 64, kHeld, kHalfTile>(a, stream);
         case 128: 
-            return a.of_tile == kFullTile ? tile_one<T, 128, kE4m3, kFullTile>(a, stream)
-                                          : tile_one<T, 128, kE4m3, kHalfTile>(a, stream);
-        default: return tile_one<T, 256, kE4m3, kHalfTile>(a, stream);
+            return a.of_tile == kFullTile ? tile_one<T, 128, kHeld, kFullTile>(a, stream)
+                                          : tile_one<T, 128, kHeld, kHalfTile>(a, stream);
+        default: return tile_one<T, 256, kHeld, kHalfTile>(a, stream);
+    }
+}
+
+template <class T>
+hipError_t tile_held(const AttentionArgs& a, uint32_t dim, Held held, hipStream_t stream) {
+    switch (held) {
+        case kHalves: return tile_dim<T, kHalves>(a, dim, stream);
+        case kE4m3Rows: return tile_dim<T, kE4m3Rows>(a, dim, stream);
+        case kE4m3Pages: return tile_dim<T, kE4m3Pages>(a, dim, stream);
+        default: return tile_dim<T, kI8Pages>(a, dim, stream);
     }
 }
 
 }  // namespace
 
-hipError_t launch_paged_tile(const AttentionArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream) {
-    if (type == ENGRAM_BF16) return e4m3 ? tile_dim<Bf16, true>(a, dim, stream) : tile_dim<Bf16, false>(a, dim, stream);
-    return e4m3 ? tile_dim<F16, true>(a, dim, stream) : tile_dim<F16, false>(a, dim, stream);
+hipError_t launch_paged_tile(const AttentionArgs& a, uint32_t dim, uint32_t type, Held held, hipStream_t stream) {
+    return type == ENGRAM_BF16 ? tile_held<Bf16>(a, dim, held, stream) : tile_held<F16>(a, dim, held, stream);
 }
 
 }  // namespace engram

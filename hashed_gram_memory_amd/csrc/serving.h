@@ -64,6 +64,13 @@ struct Bf16 : Halves<0x7F80u, 0x3F80u> {
     static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, kHigh));
     }
+    // two int8 codes likewise: their floats have no digits below this type's
+    template <bool kHigh>
+    static __device__ __forceinline__ uint32_t from_i8(uint32_t w) {
+        const float a = static_cast<float>(static_cast<int8_t>(w >> (kHigh ? 16 : 0)));
+        const float b = static_cast<float>(static_cast<int8_t>(w >> (kHigh ? 24 : 8)));
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+    }
     // Softmax terms are held as 2^kShift at their row's reference, and may pass
     // it by 2^kSlack before the reference moves.
     static constexpr float kShift = 0.0f, kSlack = 8.0f;
@@ -92,10 +99,30 @@ struct F16 : Halves<0x7C00u, 0x3C00u> {
     static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, kHigh));
     }
+    // 1,024 + 128 + the code by its bits, less 1,152: both exact
+    template <bool kHigh>
+    static __device__ __forceinline__ uint32_t from_i8(uint32_t w) {
+        const uint32_t x = __builtin_amdgcn_perm(w ^ 0x80808080u, 0x64646464u, kHigh ? 0x00070006u : 0x00050004u);
+        const f16x2v off = {static_cast<_Float16>(1152.0f), static_cast<_Float16>(1152.0f)};
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2v, x) - off);
+    }
     // fp16 ends at 65,504 and has all its digits down to 2^-14: with a term of
     // 2^14 at most, one of 2^-21 of the reference is still a normal number.
     static constexpr float kShift = 7.0f, kSlack = 7.0f;
 };
+
+// What a cache holds: 16-bit numbers, or codes with a scale for each row (e4m3)
+// or for each page and head (e4m3, int8).
+enum Held : int { kHalves, kE4m3Rows, kE4m3Pages, kI8Pages };
+
+// Two codes (bytes 0 and 1, or 2 and 3, of w) as numbers of type T, exactly.
+template <class T, int kHeld, bool kHigh>
+__device__ __forceinline__ uint32_t from_codes(uint32_t w) {
+    if constexpr (kHeld == kI8Pages)
+        return T::template from_i8<kHigh>(w);
+    else
+        return T::template from_e4m3<kHigh>(w);
+}
 
 // The larger, and the sum, of a lane's value and that of the lane 16 (32) away.
 __device__ __forceinline__ f32x2v swap16(float x) {
@@ -126,8 +153,9 @@ __device__ __forceinline__ float sum32(float x) {
 }
 
 // The paged cache as the kernels see it: K and V each [n_pages][n_kv_heads]
-// [page][dim], page p starting at p * page_stride elements; an e4m3 cache
-// also has one fp32 scale for each (page, head, slot).  page is 2^page_shift.
+// [page][dim], page p starting at p * page_stride elements; a cache of codes
+// also has one fp32 scale for each (page, head, slot) or for each (page, head).
+// page is 2^page_shift.
 struct CacheView {
     uint8_t* k;
     uint8_t* v;
@@ -168,6 +196,29 @@ struct AppendArgs {
     float eps;
 };
 
+// As AppendArgs, to pages with one scale each: the tokens of a request are the last of its kv_len keys.
+struct AppendPagesArgs {
+    const uint8_t* src[2];  // k and v
+    int64_t src_tok[2], src_head[2];
+    const uint8_t* weight;
+    const int32_t* positions;
+    const double* inv_freq;
+    const int32_t* table;   // [n_seq][table_width], row stride table_stride
+    const int32_t* kv_len;  // [n_seq]
+    const int32_t* cu_q;    // [n_seq + 1], or nullptr: uniform_q tokens each
+    CacheView cache;
+    int64_t table_stride;
+    uint32_t table_width;
+    uint32_t n_seq, n_tok;
+    uint32_t uniform_q;
+    uint32_t most_q;        // tokens of a request at most; 0: not known
+    uint32_t pages_per;     // pages set aside for each request; 0: as the lengths need
+    uint32_t rotary;
+    uint32_t interleaved;
+    float eps;
+};
+
+hipError_t launch_append_pages(const AppendPagesArgs& a, uint32_t dim, uint32_t type, bool int8, hipStream_t stream);
 hipError_t launch_norm_rope(const NormRopeArgs& a, uint32_t dim, uint32_t type, hipStream_t stream);
 hipError_t launch_append(const AppendArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);
 

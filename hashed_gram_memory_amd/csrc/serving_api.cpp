@@ -1,4 +1,4 @@
-// Host side of the serving calls (head norm + rotation, cache append, paged
+// Host side of the serving calls (head norm + rotation, cache appends, paged
 // attention): validation, the split of the keys, launches.  As in
 // engram_api.cpp, every argument is checked before anything is launched and
 // nothing here synchronises or allocates device memory.
@@ -14,6 +14,7 @@ namespace {
 
 bool good_dim(uint32_t d) { return d == 64 || d == 128 || d == 256; }
 bool good_type(uint32_t t) { return t == ENGRAM_BF16 || t == ENGRAM_F16; }
+bool of_pages(uint32_t t) { return t == ENGRAM_E4M3_PAGE || t == ENGRAM_I8_PAGE; }  // codes with a scale for each page
 
 // Strides of a [tokens][heads][dim] tensor: whole 16-byte blocks, not negative.
 bool good_strides(int64_t tok, int64_t head) {
@@ -32,7 +33,8 @@ int check_rotation(uint32_t rotary, uint32_t dim, int64_t n_tok, const int32_t* 
 
 int view_of(const engram_kv_cache* c, CacheView* out) {
     if (!c) return ENGRAM_EINVAL;
-    if (c->type != ENGRAM_BF16 && c->type != ENGRAM_F16 && c->type != ENGRAM_E4M3) return ENGRAM_EUNSUPPORTED;
+    const bool coded = c->type == ENGRAM_E4M3 || of_pages(c->type);
+    if (!good_type(c->type) && !coded) return ENGRAM_EUNSUPPORTED;
     if (!good_dim(c->head_dim)) return ENGRAM_EUNSUPPORTED;
     const uint32_t p = c->page_size;
     if (p < 8 || p > 1024 || (p & (p - 1)) != 0) return ENGRAM_EUNSUPPORTED;
@@ -42,8 +44,7 @@ int view_of(const engram_kv_cache* c, CacheView* out) {
     const int64_t most = INT64_MAX / 2 / c->n_pages;
     for (int64_t s : {c->k_page_stride, c->v_page_stride})
         if (s < inner || s % 16 != 0 || s > most) return ENGRAM_EINVAL;
-    if (c->type == ENGRAM_E4M3 &&
-        (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
+    if (coded && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
         return ENGRAM_EINVAL;
     out->k = static_cast<uint8_t*>(c->k);
     out->v = static_cast<uint8_t*>(c->v);
@@ -111,7 +112,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     const int st = view_of(d->cache, &view);
     if (st != ENGRAM_OK) return st;
     if (!good_type(d->type)) return ENGRAM_EUNSUPPORTED;
-    if (d->cache->type != ENGRAM_E4M3 && d->cache->type != d->type) return ENGRAM_EUNSUPPORTED;
+    if (good_type(d->cache->type) && d->cache->type != d->type) return ENGRAM_EUNSUPPORTED;
     if (d->n_seq < 0 || d->n_tok < 0 || d->table_width < 0 || d->max_q_len < 0 || d->window < 0) return ENGRAM_EINVAL;
     if (d->n_q_heads == 0 || d->n_q_heads > 65535 || d->n_q_heads % d->cache->n_kv_heads != 0) return ENGRAM_EINVAL;
     if (d->reserved0 != 0) return ENGRAM_EINVAL;
@@ -193,7 +194,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         const int64_t keys = keys_of(f.max_rows, 32);
         const int64_t blocks = (keys + kRowsBlock - 1) / kRowsBlock;
         const bool whole = blocks * d->cache->head_dim <= 512 || (groups >= 512 && blocks <= 8) || groups * blocks >> 31;
-        const bool two = groups > 64 || (d->cache->type == ENGRAM_E4M3 && d->cache->head_dim < 256);
+        const bool two = groups > 64 || (!good_type(d->cache->type) && d->cache->head_dim < 256);
         f.n_work = whole ? 0u : static_cast<uint32_t>(std::min<uint64_t>(groups * blocks, two ? 512 : 256));
         if (f.n_work) {
             const size_t rows = size_t(f.n_work) * 2 * std::min(f.max_rows, kRowsTile);
@@ -320,6 +321,64 @@ int engram_kv_append(const engram_append_desc* d, void* stream) {
     return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
 }
 
+int engram_kv_append_pages(const engram_append_pages_desc* d, void* stream) {
+    if (!d) return ENGRAM_EINVAL;
+    AppendPagesArgs a;
+    int st = view_of(d->cache, &a.cache);
+    if (st != ENGRAM_OK) return st;
+    if (!good_type(d->type) || !of_pages(d->cache->type)) return ENGRAM_EUNSUPPORTED;
+    if (d->n_seq < 0 || d->n_tok < 0 || d->table_width < 0 || d->max_q_len < 0 || d->reserved0 != 0) return ENGRAM_EINVAL;
+    if (d->n_tok > INT32_MAX || d->n_seq > (1 << 24) || d->table_width > INT32_MAX) return ENGRAM_ERANGE;
+    st = check_rotation(d->rotary_dim, d->cache->head_dim, d->n_tok, d->positions, d->inv_freq, d->interleaved, d->eps);
+    if (st != ENGRAM_OK) return st;
+    if (d->n_tok == 0) return ENGRAM_OK;
+    if (d->n_seq == 0) return ENGRAM_EINVAL;
+    if (!d->cu_q && d->n_tok % d->n_seq != 0) return ENGRAM_EINVAL;
+    if (!d->k || !d->v || !d->kv_len || !aligned(d->k, 16) || !aligned(d->v, 16) || !aligned(d->kv_len, 4) ||
+        !aligned(d->cu_q, 4) || !aligned(d->k_weight, 16))
+        return ENGRAM_EINVAL;
+    if (!good_strides(d->k_token_stride, d->k_head_stride) || !good_strides(d->v_token_stride, d->v_head_stride))
+        return ENGRAM_EINVAL;
+    if (d->table_stride < 0 || d->table_stride > (int64_t(1) << 40)) return ENGRAM_EINVAL;
+    if (d->table_width == 0) return ENGRAM_OK;  // no request has a page
+    if (!d->block_table || !aligned(d->block_table, 4) || d->table_stride < d->table_width) return ENGRAM_EINVAL;
+    a.src[0] = static_cast<const uint8_t*>(d->k);
+    a.src[1] = static_cast<const uint8_t*>(d->v);
+    a.src_tok[0] = d->k_token_stride;
+    a.src_head[0] = d->k_head_stride;
+    a.src_tok[1] = d->v_token_stride;
+    a.src_head[1] = d->v_head_stride;
+    a.weight = static_cast<const uint8_t*>(d->k_weight);
+    a.positions = d->positions;
+    a.inv_freq = d->inv_freq;
+    a.table = d->block_table;
+    a.kv_len = d->kv_len;
+    a.cu_q = d->cu_q;
+    a.table_stride = d->table_stride;
+    a.table_width = static_cast<uint32_t>(d->table_width);
+    a.n_seq = static_cast<uint32_t>(d->n_seq);
+    a.n_tok = static_cast<uint32_t>(d->n_tok);
+    a.uniform_q = d->cu_q ? 0u : static_cast<uint32_t>(d->n_tok / d->n_seq);
+    const uint64_t bound = d->cu_q ? (d->max_q_len ? std::min<uint64_t>(d->max_q_len, a.n_tok) : d->n_seq == 1 ? a.n_tok : 0)
+                                   : a.uniform_q;
+    a.most_q = static_cast<uint32_t>(bound);
+    // A run of n tokens touches at most (n + page - 2) / page + 1 pages; set aside for each request where that is fewer than
+    // room for any lengths.
+    const uint64_t page = uint64_t(1) << a.cache.page_shift, any = (a.n_tok >> a.cache.page_shift) + 2 * uint64_t(a.n_seq);
+    const uint64_t per = bound ? (bound + page - 2) / page + 1 : 0;
+    const bool each = per && (per * a.n_seq <= any || !d->cu_q);
+    a.pages_per = each ? static_cast<uint32_t>(per) : 0u;
+    // workgroups of 256 threads, and a grid has less than 2^32
+    if ((each ? per * a.n_seq : any) * ((2 * uint64_t(a.cache.n_kv_heads) + 15) / 16) >> 23) return ENGRAM_ERANGE;
+    if (bound == 1 && uint64_t(a.n_seq) * 2 * a.cache.n_kv_heads >> 24) return ENGRAM_ERANGE;
+    a.rotary = d->rotary_dim;
+    a.interleaved = d->interleaved;
+    a.eps = d->eps;
+    const hipError_t e = launch_append_pages(a, d->cache->head_dim, d->type, d->cache->type == ENGRAM_I8_PAGE,
+                                             static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
+}
+
 int engram_paged_attention_workspace(const engram_attention_desc* d, size_t* bytes) {
     if (!bytes) return ENGRAM_EINVAL;
     Launches l;
@@ -347,13 +406,16 @@ int engram_paged_attention(const engram_attention_desc* d, void* ws, size_t ws_b
     }
     const hipStream_t to = static_cast<hipStream_t>(stream);
     const uint32_t dim = d->cache->head_dim;
-    const bool e4m3 = d->cache->type == ENGRAM_E4M3;
+    const Held held = d->cache->type == ENGRAM_E4M3        ? kE4m3Rows
+                      : d->cache->type == ENGRAM_E4M3_PAGE ? kE4m3Pages
+                      : d->cache->type == ENGRAM_I8_PAGE   ? kI8Pages
+                                                           : kHalves;
     hipError_t e = hipSuccess;
     if (l.any_many) {
-        e = launch_paged_tile(l.many, dim, d->type, e4m3, to);
+        e = launch_paged_tile(l.many, dim, d->type, held, to);
         if (e == hipSuccess && l.many.n_split > 1) e = launch_paged_join(l.many, dim, d->type, to);
     }
-    if (e == hipSuccess && l.any_few) e = launch_paged_rows(l.few, dim, d->type, e4m3, to);
+    if (e == hipSuccess && l.any_few) e = launch_paged_rows(l.few, dim, d->type, held, to);
     return e == hipSuccess ? ENGRAM_OK : ENGRAM_EHIP;
 }
 

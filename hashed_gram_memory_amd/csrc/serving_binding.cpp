@@ -156,8 +156,9 @@ engram_kv_cache cache_of(const Args& a, int k_at, int v_at, int k_scale, int v_s
     for (int s = 0; s < 2; ++s) {
         const at::Tensor& x = a.on_device(s ? v_at : k_at, names[s]);
         const auto type = x.scalar_type();
-        if (x.dim() != 4 || (type != at::kBFloat16 && type != at::kHalf && type != at::kByte && type != at::kFloat8_e4m3fn))
-            refuse(std::string(names[s]) + " must be a bfloat16, float16, uint8 or float8_e4m3fn tensor "
+        if (x.dim() != 4 || (type != at::kBFloat16 && type != at::kHalf && type != at::kByte && type != at::kFloat8_e4m3fn &&
+                             type != at::kChar))
+            refuse(std::string(names[s]) + " must be a bfloat16, float16, uint8, float8_e4m3fn or int8 tensor "
                    "[n_pages, n_kv_heads, page_size, head_dim], got " + shape_of(x));
         const int64_t h = x.size(1), p = x.size(2), d = x.size(3);
         if ((x.stride(3) != 1 && d > 1) || (x.stride(2) != d && p > 1) || (x.stride(1) != p * d && h > 1))
@@ -168,19 +169,23 @@ engram_kv_cache cache_of(const Args& a, int k_at, int v_at, int k_scale, int v_s
     if (t[0]->sizes() != t[1]->sizes() || t[0]->scalar_type() != t[1]->scalar_type())
         refuse("k_cache and v_cache must have the same shape and type");
     const auto type = t[0]->scalar_type();
-    c.type = type == at::kBFloat16 ? ENGRAM_BF16 : type == at::kHalf ? ENGRAM_F16 : ENGRAM_E4M3;
-    if (c.type == ENGRAM_E4M3) {
+    c.type = type == at::kBFloat16 ? ENGRAM_BF16 : type == at::kHalf ? ENGRAM_F16 : type == at::kChar ? ENGRAM_I8_PAGE : ENGRAM_E4M3;
+    if (c.type == ENGRAM_E4M3 || c.type == ENGRAM_I8_PAGE) {
+        // a scale for each page and head, or (e4m3) for each row
+        if (c.type == ENGRAM_E4M3 && a.given(k_scale) && a.tensor(k_scale, "k_scale").dim() == 2) c.type = ENGRAM_E4M3_PAGE;
+        const bool rows = c.type == ENGRAM_E4M3;
         for (int s = 0; s < 2; ++s) {
             const int i = s ? v_scale : k_scale;
             const char* name = s ? "v_scale" : "k_scale";
-            if (!a.given(i)) refuse(std::string("an e4m3 cache needs ") + name);
+            if (!a.given(i)) refuse(std::string(rows ? "an e4m3 cache needs " : "a cache of codes needs ") + name);
             const at::Tensor& x = a.on_device(i, name);
-            if (x.scalar_type() != at::kFloat || x.sizes() != t[0]->sizes().slice(0, 3) || !x.is_contiguous())
-                refuse(std::string(name) + " must be a contiguous float32 [n_pages, n_kv_heads, page_size]");
+            if (x.scalar_type() != at::kFloat || x.sizes() != t[0]->sizes().slice(0, rows ? 3 : 2) || !x.is_contiguous())
+                refuse(std::string(name) + " must be a contiguous float32 [n_pages, n_kv_heads" + (rows ? ", page_size]" : "]") +
+                       ", got " + shape_of(x));
             (s ? c.v_scale : c.k_scale) = static_cast<float*>(x.data_ptr());
         }
     } else if (a.given(k_scale) || a.given(v_scale)) {
-        refuse("k_scale and v_scale belong to an e4m3 cache");
+        refuse("k_scale and v_scale belong to a cache of codes");
     }
     const auto u32 = [](int64_t x) { return static_cast<uint32_t>(std::min<int64_t>(x, UINT32_MAX)); };
     c.k = t[0]->data_ptr();
@@ -192,6 +197,13 @@ engram_kv_cache cache_of(const Args& a, int k_at, int v_at, int k_scale, int v_s
     c.page_size = u32(t[0]->size(2));
     c.head_dim = u32(t[0]->size(3));
     return c;
+}
+
+const at::Tensor& table_of(const Args& a, int i) {
+    const at::Tensor& t = a.on_device(i, "block_table");
+    if (t.scalar_type() != at::kInt || t.dim() != 2) refuse("block_table must be int32 [n_seq, width]");
+    if (t.size(1) > 1 && t.stride(1) != 1) refuse("block_table must be contiguous along its width");
+    return t;
 }
 
 void check(int status, const char* what) {
@@ -225,6 +237,41 @@ void launch(const Args& a, const char* what, F f) {
     st = f(stream);
     Py_END_ALLOW_THREADS
     check(st, what);
+}
+
+// A call's workspace: the one given, or one allocated for `need` bytes.
+struct Workspace {
+    at::Tensor held;
+    void* p = nullptr;
+    size_t bytes = 0;
+};
+Workspace workspace_of(const Args& a, int i, size_t need) {
+    Workspace w;
+    if (a.given(i)) {
+        const at::Tensor& t = a.on_device(i, "workspace");
+        if (t.scalar_type() != at::kByte || !t.is_contiguous()) refuse("workspace must be a contiguous uint8 tensor");
+        w.p = t.data_ptr();
+        w.bytes = static_cast<size_t>(t.numel());
+    } else if (need) {
+        w.held = at::empty({static_cast<int64_t>(need)}, at::TensorOptions().device(a.device).dtype(at::kByte));
+        w.p = w.held.data_ptr();
+        w.bytes = need;
+    }
+    return w;
+}
+
+PyObject* pack(std::initializer_list<at::Tensor> tensors) {
+    PyObject* all = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
+    Py_ssize_t at = 0;
+    for (const at::Tensor& t : tensors) {
+        PyObject* x = all ? THPVariable_Wrap(t) : nullptr;
+        if (!x) {
+            Py_XDECREF(all);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(all, at++, x);
+    }
+    return all;
 }
 
 template <class F>
@@ -325,6 +372,8 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
         Args a{args};
         const at::Tensor& k = a.lead(0, "k");
         const engram_kv_cache c = cache_of(a, 2, 3, 10, 11);
+        if (c.type == ENGRAM_E4M3_PAGE || c.type == ENGRAM_I8_PAGE)
+            refuse("a cache with a scale for each page and head takes kv_append_pages");
         const Rows kr = rows_of(a, 0, "k", c.head_dim), vr = rows_of(a, 1, "v", c.head_dim);
         if (a.tensor(1, "v").sizes() != k.sizes() || k.size(1) != c.n_kv_heads)
             refuse("k and v must be [n_tok, " + std::to_string(c.n_kv_heads) + ", " + std::to_string(c.head_dim) + "]");
@@ -360,9 +409,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
         const bool size_only = a.truth(14);
         const engram_kv_cache c = cache_of(a, 1, 2, 9, 10);
         const Rows qr = rows_of(a, 0, "q", c.head_dim);
-        const at::Tensor& table = a.on_device(3, "block_table");
-        if (table.scalar_type() != at::kInt || table.dim() != 2) refuse("block_table must be int32 [n_seq, width]");
-        if (table.size(1) > 1 && table.stride(1) != 1) refuse("block_table must be contiguous along its width");
+        const at::Tensor& table = table_of(a, 3);
         engram_attention_desc d = {};
         d.cache = &c;
         d.q = qr.p;
@@ -400,26 +447,160 @@ PyObject* paged_attention(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
         size_t need = 0;
         check(engram_paged_attention_workspace(&d, &need), "engram_paged_attention_workspace");
         if (size_only) return PyLong_FromSize_t(need);
-        at::Tensor held;
-        void* ws = nullptr;
-        size_t ws_bytes = 0;
-        if (a.given(13)) {
-            const at::Tensor& w = a.on_device(13, "workspace");
-            if (w.scalar_type() != at::kByte || !w.is_contiguous()) refuse("workspace must be a contiguous uint8 tensor");
-            ws = w.data_ptr();
-            ws_bytes = static_cast<size_t>(w.numel());
-        } else if (need) {
-            held = at::empty({static_cast<int64_t>(need)}, q.options().dtype(at::kByte).requires_grad(false));
-            ws = held.data_ptr();
-            ws_bytes = need;
-        }
-        launch(a, "engram_paged_attention", [&](void* stream) { return engram_paged_attention(&d, ws, ws_bytes, stream); });
+        const Workspace ws = workspace_of(a, 13, need);
+        launch(a, "engram_paged_attention", [&](void* stream) { return engram_paged_attention(&d, ws.p, ws.bytes, stream); });
         if (!lse.defined()) return THPVariable_Wrap(out);
-        PyObject* both[2] = {THPVariable_Wrap(out), THPVariable_Wrap(lse)};
-        PyObject* pair = both[0] && both[1] ? PyTuple_Pack(2, both[0], both[1]) : nullptr;
-        Py_XDECREF(both[0]);
-        Py_XDECREF(both[1]);
-        return pair;
+        return pack({out, lse});
+    });
+}
+
+// k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, cu_q, max_q_len, positions, inv_freq, k_weight, eps, interleaved
+PyObject* kv_append_pages(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+    return guarded(n_args, 15, [&]() -> PyObject* {
+        Args a{args};
+        const at::Tensor& k = a.lead(0, "k");
+        const engram_kv_cache c = cache_of(a, 2, 3, 4, 5);
+        if (c.type != ENGRAM_E4M3_PAGE && c.type != ENGRAM_I8_PAGE)
+            refuse("kv_append_pages wants a cache of codes with scales [n_pages, n_kv_heads]");
+        const Rows kr = rows_of(a, 0, "k", c.head_dim), vr = rows_of(a, 1, "v", c.head_dim);
+        if (a.tensor(1, "v").sizes() != k.sizes() || k.size(1) != c.n_kv_heads)
+            refuse("k and v must be [n_tok, " + std::to_string(c.n_kv_heads) + ", " + std::to_string(c.head_dim) + "]");
+        const at::Tensor& table = table_of(a, 6);
+        engram_append_pages_desc d = {};
+        d.cache = &c;
+        d.k = kr.p;
+        d.v = vr.p;
+        d.n_tok = k.size(0);
+        d.n_seq = table.size(0);
+        d.block_table = static_cast<const int32_t*>(table.data_ptr());
+        d.kv_len = static_cast<const int32_t*>(needed(a, 7, "kv_len", at::kInt, d.n_seq));
+        d.cu_q = static_cast<const int32_t*>(vector_of(a, 8, "cu_q", at::kInt, d.n_seq + 1));
+        d.max_q_len = a.given(9) ? a.number(9) : 0;
+        d.table_width = table.size(1);
+        d.table_stride = d.n_seq > 1 ? table.stride(0) : d.table_width;
+        d.k_weight = vector_of(a, 12, "k_weight", a.type, c.head_dim);
+        const Rotation r = rotation_of(a, 10, 11, d.n_tok);
+        d.positions = r.positions;
+        d.inv_freq = r.inv_freq;
+        d.rotary_dim = r.dim;
+        d.k_token_stride = kr.tok;
+        d.k_head_stride = kr.head;
+        d.v_token_stride = vr.tok;
+        d.v_head_stride = vr.head;
+        d.eps = static_cast<float>(a.real(13));
+        d.interleaved = a.truth(14);
+        d.type = a.kind();
+        launch(a, "engram_kv_append_pages", [&](void* stream) { return engram_kv_append_pages(&d, stream); });
+        Py_RETURN_NONE;
+    });
+}
+
+// lengths, new_tokens, block_table, held, free_pages, n_free, page_size, n_tok, workspace, size_only
+PyObject* page_tables(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+    return guarded(n_args, 10, [&]() -> PyObject* {
+        Args a{args};
+        a.device = a.tensor(2, "block_table").device();
+        const at::Tensor& table = table_of(a, 2);
+        engram_page_tables_desc d = {};
+        d.n_seq = table.size(0);
+        d.table_width = table.size(1);
+        d.table_stride = d.n_seq > 1 ? table.stride(0) : d.table_width;
+        d.block_table = static_cast<int32_t*>(table.data_ptr());
+        d.lengths = static_cast<const int32_t*>(needed(a, 0, "lengths", at::kInt, d.n_seq));
+        d.new_tokens = static_cast<const int32_t*>(vector_of(a, 1, "new_tokens", at::kInt, d.n_seq));
+        d.held = static_cast<int32_t*>(needed(a, 3, "held", at::kInt, d.n_seq));
+        const at::Tensor& stack = a.on_device(4, "free_pages");
+        if (stack.scalar_type() != at::kInt || stack.dim() != 1 || !stack.is_contiguous())
+            refuse("free_pages must be a contiguous int32 [n_pages], got " + shape_of(stack));
+        d.free_pages = static_cast<int32_t*>(stack.data_ptr());
+        d.n_pages = stack.size(0);
+        d.n_free = static_cast<int32_t*>(needed(a, 5, "n_free", at::kInt, 1));
+        const long long page = a.number(6);
+        d.page_size = page > 0 && page <= UINT32_MAX ? static_cast<uint32_t>(page) : 0u;
+        d.n_tok = a.number(7);
+        if (d.n_tok < 0) refuse("n_tok is negative");
+        const bool size_only = a.truth(9);
+        const auto ints = table.options();
+        at::Tensor slots, positions, cu_q, kv_len, n_short;
+        static int64_t nothing[2];  // stands for outputs that are not there yet, where only their sizes are looked at
+        if (size_only) {
+            d.slots = nothing;
+            d.positions = d.cu_q = d.kv_len = d.n_short = reinterpret_cast<int32_t*>(nothing);
+        } else {
+            slots = at::empty({d.n_tok}, ints.dtype(at::kLong));
+            positions = at::empty({d.n_tok}, ints);
+            cu_q = at::empty({d.n_seq + 1}, ints);
+            kv_len = at::empty({d.n_seq}, ints);
+            n_short = at::empty({1}, ints);
+            d.slots = static_cast<int64_t*>(slots.data_ptr());
+            d.positions = static_cast<int32_t*>(positions.data_ptr());
+            d.cu_q = static_cast<int32_t*>(cu_q.data_ptr());
+            d.kv_len = static_cast<int32_t*>(kv_len.data_ptr());
+            d.n_short = static_cast<int32_t*>(n_short.data_ptr());
+        }
+        size_t need = 0;
+        check(engram_page_tables_workspace(&d, &need), "engram_page_tables_workspace");
+        if (size_only) return PyLong_FromSize_t(need);
+        const Workspace ws = workspace_of(a, 8, need);
+        launch(a, "engram_page_tables", [&](void* stream) { return engram_page_tables(&d, ws.p, ws.bytes, stream); });
+        return pack({slots, positions, cu_q, kv_len, n_short});
+    });
+}
+
+// target, draft, uniform, last_uniform, draft_probs, cu_draft, workspace, size_only
+PyObject* verify_draft(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+    return guarded(n_args, 8, [&]() -> PyObject* {
+        Args a{args};
+        a.device = a.tensor(0, "target").device();
+        engram_verify_draft_desc d = {};
+        const auto rows = [&](int i, const char* name, at::ScalarType type) -> const at::Tensor& {
+            const at::Tensor& t = a.on_device(i, name);
+            if (t.scalar_type() != type || t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1))
+                refuse(std::string(name) + " must be [rows, vocab] of " + c10::toString(type) + ", contiguous along vocab, got " +
+                       shape_of(t));
+            return t;
+        };
+        const auto type = a.tensor(0, "target").scalar_type();
+        if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
+            refuse(std::string("target must be float32, bfloat16 or float16, got ") + c10::toString(type));
+        const at::Tensor& p = rows(0, "target", type);
+        const at::Tensor& draft = a.on_device(1, "draft");
+        if (draft.dim() != 1) refuse("draft must be int32 [n_draft], got " + shape_of(draft));
+        d.n_draft = draft.size(0);
+        d.n_seq = p.size(0) - d.n_draft;
+        if (d.n_seq < 0) refuse("target must have a row for each draft and one more for each request");
+        d.vocab = p.size(1);
+        d.target = p.data_ptr();
+        d.target_stride = p.size(0) > 1 ? p.stride(0) : 0;
+        d.type = type == at::kFloat ? ENGRAM_F32 : type == at::kBFloat16 ? ENGRAM_BF16 : ENGRAM_F16;
+        d.draft = static_cast<const int32_t*>(needed(a, 1, "draft", at::kInt, d.n_draft));
+        d.uniform = static_cast<const float*>(needed(a, 2, "uniform", at::kFloat, d.n_draft));
+        d.last_uniform = static_cast<const float*>(needed(a, 3, "last_uniform", at::kFloat, d.n_seq));
+        if (a.given(4)) {
+            const at::Tensor& q = rows(4, "draft_probs", type);
+            if (q.size(0) != d.n_draft || q.size(1) != d.vocab)
+                refuse("draft_probs must be [" + std::to_string(d.n_draft) + ", " + std::to_string(d.vocab) + "], got " + shape_of(q));
+            d.draft_probs = q.data_ptr();
+            d.draft_stride = q.size(0) > 1 ? q.stride(0) : 0;
+        }
+        d.cu_draft = static_cast<const int32_t*>(vector_of(a, 5, "cu_draft", at::kInt, d.n_seq + 1));
+        const bool size_only = a.truth(7);
+        at::Tensor tokens, accepted;
+        static int32_t nothing[1];  // stands for outputs that are not there yet
+        if (size_only) {
+            d.tokens = d.n_accepted = nothing;
+        } else {
+            tokens = at::empty({p.size(0)}, draft.options());
+            accepted = at::empty({d.n_seq}, draft.options());
+            d.tokens = static_cast<int32_t*>(tokens.data_ptr());
+            d.n_accepted = static_cast<int32_t*>(accepted.data_ptr());
+        }
+        size_t need = 0;
+        check(engram_verify_draft_workspace(&d, &need), "engram_verify_draft_workspace");
+        if (size_only) return PyLong_FromSize_t(need);
+        const Workspace ws = workspace_of(a, 6, need);
+        launch(a, "engram_verify_draft", [&](void* stream) { return engram_verify_draft(&d, ws.p, ws.bytes, stream); });
+        return pack({tokens, accepted});
     });
 }
 
@@ -435,7 +616,8 @@ PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
 }
 
 #define ENGRAM_FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {ENGRAM_FAST(qk_norm_rope), ENGRAM_FAST(kv_append), ENGRAM_FAST(paged_attention), ENGRAM_FAST(setup),
+PyMethodDef g_methods[] = {ENGRAM_FAST(qk_norm_rope), ENGRAM_FAST(kv_append), ENGRAM_FAST(paged_attention),
+                           ENGRAM_FAST(kv_append_pages), ENGRAM_FAST(page_tables), ENGRAM_FAST(verify_draft), ENGRAM_FAST(setup),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

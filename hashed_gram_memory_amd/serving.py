@@ -1,16 +1,23 @@
-"""Serving operators next to the lookup: head norm + rotation, paged cache append, paged attention.
+"""Serving operators next to the lookup: head norm + rotation, paged cache appends, paged attention, and between the steps
+page tables, slots and the verification of drafts.
 
 Argument marshalling only, as in the package's own module; the C ABI is in
 include/engram.h.  A cache is a pair of device tensors [n_pages, n_kv_heads,
-page_size, head_dim] that the caller owns: bfloat16 or float16, or FP8 E4M3
-codes (uint8 or float8_e4m3fn) with float32 scales [n_pages, n_kv_heads,
-page_size] for K and V.
+page_size, head_dim] that the caller owns: bfloat16 or float16, or codes with
+float32 scales for K and V: FP8 E4M3 (uint8 or float8_e4m3fn) with scales
+[n_pages, n_kv_heads, page_size] or [n_pages, n_kv_heads], int8 with the latter.
 
     q, _ = qk_norm_rope(q, None, positions, inv_freq, q_weight=wq)       # engram_qk_norm_rope
     kv_append(k, v, k_cache, v_cache, slots, positions=positions, inv_freq=inv_freq, k_weight=wk)  # engram_kv_append
     out = paged_attention(q, k_cache, v_cache, block_table, kv_len)       # engram_paged_attention
 
-attention_example.py runs them together, next to the lookup.
+A batch that goes on by itself, with a cache of one scale for each page and head:
+
+    slots, positions, cu_q, kv_len, n_short = page_tables(lengths, new, block_table, held, free_pages, n_free, page_size, n_tok)
+    kv_append_pages(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, cu_q, ...)  # engram_kv_append_pages
+    tokens, n_accepted = verify_draft(target, draft, uniform, last_uniform, draft_probs)  # engram_verify_draft
+
+attention_example.py runs the first together, next to the lookup, drafting_example.py all of them.
 
 The operators serve: they have no backward, and refuse tensors that require
 a gradient while gradients are recorded, and those with a forward gradient.  They run on the current stream of
@@ -30,7 +37,7 @@ import hashed_gram_memory_amd as _hg
 
 _VP, _I64, _U32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
 
-BF16, F16, E4M3 = 0, 1, 2
+BF16, F16, E4M3, E4M3_PAGE, I8_PAGE, F32 = 0, 1, 2, 4, 5, 6
 
 
 class KvCacheDesc(ctypes.Structure):
@@ -63,8 +70,32 @@ class AttentionDesc(ctypes.Structure):
                 ("type", _U32), ("scale", _F32), ("reserved0", _U32)]
 
 
+class AppendPagesDesc(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(KvCacheDesc)), ("k", _VP), ("v", _VP), ("k_weight", _VP), ("positions", _VP),
+                ("inv_freq", _VP), ("block_table", _VP), ("kv_len", _VP), ("cu_q", _VP), ("n_seq", _I64), ("n_tok", _I64),
+                ("max_q_len", _I64), ("table_width", _I64), ("table_stride", _I64), ("k_token_stride", _I64),
+                ("k_head_stride", _I64), ("v_token_stride", _I64), ("v_head_stride", _I64), ("rotary_dim", _U32),
+                ("interleaved", _U32), ("type", _U32), ("eps", _F32), ("reserved0", _U32)]
+
+
+class PageTablesDesc(ctypes.Structure):
+    _fields_ = [("lengths", _VP), ("new_tokens", _VP), ("block_table", _VP), ("held", _VP), ("free_pages", _VP),
+                ("n_free", _VP), ("slots", _VP), ("positions", _VP), ("cu_q", _VP), ("kv_len", _VP), ("n_short", _VP),
+                ("n_seq", _I64), ("n_tok", _I64), ("table_width", _I64), ("table_stride", _I64), ("n_pages", _I64),
+                ("page_size", _U32), ("reserved0", _U32)]
+
+
+class VerifyDraftDesc(ctypes.Structure):
+    _fields_ = [("target", _VP), ("draft_probs", _VP), ("draft", _VP), ("uniform", _VP), ("last_uniform", _VP),
+                ("cu_draft", _VP), ("tokens", _VP), ("n_accepted", _VP), ("n_seq", _I64), ("n_draft", _I64), ("vocab", _I64),
+                ("target_stride", _I64), ("draft_stride", _I64), ("type", _U32), ("reserved0", _U32)]
+
+
+_SIZE_P = ctypes.POINTER(ctypes.c_size_t)
 _lib = _hg.lib()
-for _name, _args in {"engram_qk_norm_rope": [_VP, _VP], "engram_kv_append": [_VP, _VP],
+for _name, _args in {"engram_qk_norm_rope": [_VP, _VP], "engram_kv_append": [_VP, _VP], "engram_kv_append_pages": [_VP, _VP],
+                     "engram_page_tables_workspace": [_VP, _SIZE_P], "engram_page_tables": [_VP, _VP, ctypes.c_size_t, _VP],
+                     "engram_verify_draft_workspace": [_VP, _SIZE_P], "engram_verify_draft": [_VP, _VP, ctypes.c_size_t, _VP],
                      "engram_paged_attention_workspace": [_VP, ctypes.POINTER(ctypes.c_size_t)],
                      "engram_paged_attention": [_VP, _VP, ctypes.c_size_t, _VP]}.items():
     getattr(_lib, _name).argtypes = _args
@@ -118,6 +149,80 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         return _serving.kv_append(*args)
     with _on(stream, k):
         return _serving.kv_append(*args)
+
+
+def kv_append_pages(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                    v_scale: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor | None = None,
+                    max_q_len: int | None = None, positions: torch.Tensor | None = None,
+                    inv_freq: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                    interleaved: bool = False, stream=None) -> None:
+    """kv_append for a cache of codes (e4m3, int8) with one scale for each page and head, ``k_scale`` and ``v_scale`` float32
+    [n_pages, n_kv_heads]: request b's new tokens cu_q[b] .. cu_q[b+1]-1 (None: equally many each) are the last of its
+    kv_len[b] keys, on the pages block_table[b] (engram_kv_append_pages).
+
+    A page's scale is a power of two and only grows while the page fills; codes held are rounded again when it does.  A page
+    belongs to one request.  ``max_q_len`` bounds the tokens of a request where it is known: single tokens take a smaller
+    kernel, and what is past it may be left out."""
+    args = (k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, cu_q, max_q_len, positions, inv_freq, k_weight, eps,
+            interleaved)
+    if stream is None:
+        return _serving.kv_append_pages(*args)
+    with _on(stream, k):
+        return _serving.kv_append_pages(*args)
+
+
+def page_tables(lengths: torch.Tensor, new_tokens: torch.Tensor | None, block_table: torch.Tensor, held: torch.Tensor,
+                free_pages: torch.Tensor, n_free: torch.Tensor, page_size: int, n_tok: int,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Make every request hold the pages that its length needs, and place its new tokens (engram_page_tables): (slots int64
+    [n_tok], positions int32 [n_tok], cu_q int32 [n_seq + 1], kv_len int32 [n_seq], n_short int32 [1]).
+
+    Request b has ``lengths[b]`` keys (int32 [n_seq]) and gets ``new_tokens[b]`` more (None: n_tok / n_seq each), and holds
+    the first ``held[b]`` pages of block_table[b] (int32 [n_seq, width]).  Pages past its need come back, those missing are
+    taken from what came back and then from the top of the stack ``free_pages`` [n_pages], of which ``n_free`` [1] count;
+    block_table, held, free_pages and n_free are brought up to date.  A request that cannot be served (n_short of them) keeps
+    what it holds; its tokens get slot -1 and its kv_len is 0, so that it is appended to and attended by nothing.  A request
+    of length 0 without new tokens gives back all that it holds.  ``n_tok`` is the batch's size; tokens past the requests'
+    own get slot -1.  ``workspace``: uint8 of page_tables_workspace bytes, 256-byte aligned; allocated if not given."""
+    args = (lengths, new_tokens, block_table, held, free_pages, n_free, page_size, n_tok, workspace, False)
+    if stream is None:
+        return _serving.page_tables(*args)
+    with _on(stream, block_table):
+        return _serving.page_tables(*args)
+
+
+def page_tables_workspace(lengths: torch.Tensor, new_tokens: torch.Tensor | None, block_table: torch.Tensor,
+                          held: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor, page_size: int,
+                          n_tok: int) -> int:
+    """Bytes of the workspace that page_tables needs with these arguments; it goes by their shapes and ``n_tok`` alone
+    (engram_page_tables_workspace)."""
+    return _serving.page_tables(lengths, new_tokens, block_table, held, free_pages, n_free, page_size, n_tok, None, True)
+
+
+def verify_draft(target: torch.Tensor, draft: torch.Tensor, uniform: torch.Tensor, last_uniform: torch.Tensor,
+                 draft_probs: torch.Tensor | None = None, cu_draft: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """Keep drafted tokens by the target's probabilities and draw the token after them (engram_verify_draft): (tokens int32
+    [n_draft + n_seq], n_accepted int32 [n_seq]).
+
+    Request b has the drafts cu_draft[b] .. cu_draft[b+1]-1 of ``draft`` int32 [n_draft] (None: equally many each) and one
+    row of ``target`` [n_draft + n_seq, vocab] (float32, bfloat16 or float16) more than drafts, from cu_draft[b] + b on, as
+    its tokens of ``tokens``: those accepted, the one after, then -1.  ``draft_probs`` [n_draft, vocab] are the
+    probabilities that each draft was drawn from (None: it was certain).  ``uniform`` float32 [n_draft] and ``last_uniform``
+    float32 [n_seq] are random numbers of [0, 1).  The tokens that come out are distributed as the target's own.
+    ``workspace``: uint8 of verify_draft_workspace bytes, 256-byte aligned; allocated if not given."""
+    args = (target, draft, uniform, last_uniform, draft_probs, cu_draft, workspace, False)
+    if stream is None:
+        return _serving.verify_draft(*args)
+    with _on(stream, target):
+        return _serving.verify_draft(*args)
+
+
+def verify_draft_workspace(target: torch.Tensor, draft: torch.Tensor, uniform: torch.Tensor, last_uniform: torch.Tensor,
+                           draft_probs: torch.Tensor | None = None, cu_draft: torch.Tensor | None = None) -> int:
+    """Bytes of the workspace that verify_draft needs with these arguments; it goes by their shapes alone
+    (engram_verify_draft_workspace)."""
+    return _serving.verify_draft(target, draft, uniform, last_uniform, draft_probs, cu_draft, None, True)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,

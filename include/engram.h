@@ -417,10 +417,13 @@ int engram_dedup_noalloc(engram_plan_t plan, const int32_t* ids, const int32_t* 
  * that the slices of one projection's output can be passed as they are.
  */
 
-/* Element types.  E4M3 (OCP) only as a cache's type. */
+/* Element types.  The 8-bit ones only as a cache's type, fp32 only for probabilities. */
 #define ENGRAM_BF16 0
 #define ENGRAM_F16 1
-#define ENGRAM_E4M3 2
+#define ENGRAM_E4M3 2      /* OCP, a scale for each row                  */
+#define ENGRAM_E4M3_PAGE 4 /* OCP, a scale for each page and head        */
+#define ENGRAM_I8_PAGE 5   /* int8, a scale for each page and head       */
+#define ENGRAM_F32 6
 
 /*
  * A paged cache: K and V each [n_pages][n_kv_heads][page_size][head_dim] of
@@ -428,7 +431,10 @@ int engram_dedup_noalloc(engram_plan_t plan, const int32_t* ids, const int32_t* 
  * of 16, at least one page's size; K and V may be halves of one allocation).
  * An ENGRAM_E4M3 cache holds FP8 codes and one fp32 scale for each (page,
  * head, slot), k_scale and v_scale [n_pages][n_kv_heads][page_size]: a row
- * stands for codes * scale, as a table row does.
+ * stands for codes * scale, as a table row does.  ENGRAM_E4M3_PAGE and
+ * ENGRAM_I8_PAGE have one fp32 scale for each (page, head), k_scale and
+ * v_scale [n_pages][n_kv_heads], and codes of FP8 or int8; any finite scale is
+ * read, and engram_kv_append_pages writes powers of two.
  *
  *   page_size   a power of two from 8 to 1024; head_dim 64, 128 or 256;
  *               n_kv_heads 1 to 65535; n_pages 1 to 2^31 - 1.
@@ -437,7 +443,7 @@ int engram_dedup_noalloc(engram_plan_t plan, const int32_t* ids, const int32_t* 
 typedef struct engram_kv_cache {
     void* k;
     void* v;
-    float* k_scale;               /* NULL unless ENGRAM_E4M3 */
+    float* k_scale;               /* NULL for BF16 and F16 */
     float* v_scale;
     int64_t k_page_stride;
     int64_t v_page_stride;
@@ -532,6 +538,59 @@ typedef struct engram_append_desc {
 int engram_kv_append(const engram_append_desc* desc, void* stream);
 
 /*
+ * The append for caches with a scale for each page and head (ENGRAM_E4M3_PAGE,
+ * ENGRAM_I8_PAGE).  As in the attention below, request b has the tokens
+ * cu_q[b] .. cu_q[b + 1] - 1 (cu_q NULL: n_tok / n_seq each), which are the
+ * last of its kv_len[b] keys, on the pages of block_table[b].  Keys are normed
+ * and rotated as in engram_kv_append.  For every page, head and side with new
+ * rows x (fp32, M = 448 for e4m3, 127 for int8):
+ *     need  = the least power of two (2^-126 at least) with max|x| <= need * M,
+ *             0 for a page of zeros, NaN where an x is infinite or NaN
+ *     scale = need where the first new row is the page's first, else the
+ *             larger of need and the scale held; a NaN stays
+ *     codes = x / scale, rounded to nearest, ties to even; where the scale grew,
+ *             codes of the rows held before are multiplied by old / new and
+ *             rounded again (codes under a scale that is 0 or NaN: unspecified
+ *             but for zeros under 0)
+ * Rows of a page before a request's first new token count as held, those after
+ * its last do not and are left as they are: a request whose tokens were
+ * refused appends over them.  A token before the request's first key, and one
+ * on a page number outside the pool, is left out, as are all past
+ * max_q_len (0: not known) of a request.  kv_len is bounded by table_width *
+ * page_size, by 2^31 - 4096 and by 0.  A page is written for one request:
+ * two requests of a call must not append to the same page.
+ *
+ * n_tok == 0 is a no-op.  Errors: EINVAL, ERANGE (n_tok / page_size + 2 n_seq
+ * pages times n_kv_heads / 8 above 2^23: split the batch), EUNSUPPORTED (a type
+ * or geometry other than the above).
+ */
+typedef struct engram_append_pages_desc {
+    const engram_kv_cache* cache;
+    const void* k;
+    const void* v;
+    const void* k_weight;
+    const int32_t* positions;
+    const double* inv_freq;
+    const int32_t* block_table;
+    const int32_t* kv_len;
+    const int32_t* cu_q;
+    int64_t n_seq;
+    int64_t n_tok;
+    int64_t max_q_len;
+    int64_t table_width;
+    int64_t table_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    uint32_t rotary_dim;
+    uint32_t interleaved;
+    uint32_t type;
+    float eps;
+    uint32_t reserved0;
+} engram_append_pages_desc;
+
+int engram_kv_append_pages(const engram_append_pages_desc* desc, void* stream);
+
+/*
  * Attention of new tokens over a paged cache that already holds them.
  * Request b has the q_len tokens cu_q[b] .. cu_q[b + 1] - 1 of q (cu_q NULL:
  * n_tok / n_seq each) and kv_len[b] cached keys; key j lies on page
@@ -597,6 +656,132 @@ typedef struct engram_attention_desc {
 
 int engram_paged_attention_workspace(const engram_attention_desc* desc, size_t* bytes);
 int engram_paged_attention(const engram_attention_desc* desc, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Between two steps of a batch that decodes with drafted tokens: what a
+ * server's bookkeeping would otherwise fetch to the host.  With these, a step
+ * of lookup, attention and verification can be captured and replayed while the
+ * requests grow.
+ *
+ * Page tables and slots.  Every request gets the pages that its length needs,
+ * and its new tokens their slots.  Request b has lengths[b] keys and gets
+ * new_tokens[b] more (new_tokens NULL: n_tok / n_seq each; negative numbers
+ * count as 0), and holds the first held[b] pages of block_table[b]:
+ *     need    = ceil((lengths + new_tokens) / page_size)
+ *     tokens  = cu_q[b] .. cu_q[b + 1] - 1, cu_q the sum of new_tokens before
+ *               b, n_tok at most
+ *     pool    = pages past `need` of all requests, in order of request and
+ *               place, then free_pages from free_pages[n_free - 1] down
+ * A request that holds fewer than it needs takes the pool's next pages.  Pages
+ * of the pool that came back and were not taken go on free_pages[n_free ..],
+ * in order.  A request is served unless its tokens do not all fit into n_tok,
+ * need exceeds table_width, its keys exceed 2^31 - 4096, or the pages that it
+ * and those before it take are more than the pool has (one that takes none is
+ * served all the same).  One that is not served keeps what it holds.
+ * Outputs (of served requests, tokens i = 0 .. new - 1):
+ *     slots[cu_q[b] + i]     = block_table[b][p / page_size] * page_size +
+ *                              p % page_size, p = lengths + i
+ *     positions[cu_q[b] + i] = p
+ *     kv_len[b]              = lengths + new_tokens
+ * else slot -1, position 0 and kv_len 0: the appends leave such tokens out, and
+ * the attention gives them 0.  Tokens from cu_q[n_seq] on get slot -1 too.
+ *     n_short = the number of requests that were not served
+ * block_table, held, free_pages and n_free are brought up to date; entries of a
+ * table past `held` are left as they are.
+ *
+ *   lengths, new_tokens, held, kv_len   device int32 [n_seq].  held is bounded
+ *               by 0 and table_width.
+ *   block_table device int32 [n_seq][table_width], rows table_stride apart.
+ *   free_pages  device int32 [n_pages], n_free int32 [1] (bounded by 0 and
+ *               n_pages): a stack; pages past its room are dropped.
+ *   cu_q        device int32 [n_seq + 1]; slots int64, positions int32 [n_tok];
+ *               n_short int32 [1].
+ *   page_size   a power of two from 8 to 1024.
+ *   ws          device workspace of engram_page_tables_workspace bytes
+ *               (host-only; 0 for small batches), 256-byte aligned; holds
+ *               nothing between calls; one call at a time may use it.
+ * No output may overlap another or an input.  Errors: EINVAL, ERANGE (n_seq >
+ * 2^20, n_tok >= 2^30, n_pages > 2^30), EUNSUPPORTED (page_size), EWORKSPACE.
+ */
+typedef struct engram_page_tables_desc {
+    const int32_t* lengths;
+    const int32_t* new_tokens;
+    int32_t* block_table;
+    int32_t* held;
+    int32_t* free_pages;
+    int32_t* n_free;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* cu_q;
+    int32_t* kv_len;
+    int32_t* n_short;
+    int64_t n_seq;
+    int64_t n_tok;
+    int64_t table_width;
+    int64_t table_stride;
+    int64_t n_pages;
+    uint32_t page_size;
+    uint32_t reserved0;
+} engram_page_tables_desc;
+
+int engram_page_tables_workspace(const engram_page_tables_desc* desc, size_t* bytes);
+int engram_page_tables(const engram_page_tables_desc* desc, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Verification of drafted tokens (speculative sampling): the tokens that a
+ * step emits are distributed as the target's own.  Request b has the K drafts
+ * cu_draft[b] .. cu_draft[b + 1] - 1 (cu_draft NULL: n_draft / n_seq each) and
+ * the K + 1 target rows from cu_draft[b] + b on: row i the probabilities of
+ * the token after i drafts.  With p_i a target row, q_i the drafter's
+ * probabilities that draft d_i came from, u_i in [0, 1) its random number and v in
+ * [0, 1) the request's:
+ *     a     = the first i with not (u_i * q_i(d_i) < p_i(d_i)), else K
+ *     w_j   = max(p_a(j) - q_a(j), 0) where a < K and their sum is not 0, else p_a(j)
+ *     next  = the first j with w_0 + .. + w_j > v * (w_0 + .. + w_{vocab-1})
+ *     tokens[cu_draft[b] + b ..] = d_0 .. d_{a-1}, next, then -1;  n_accepted[b] = a
+ * draft_probs NULL: the drafts were certain (q_i is 1 at d_i, 0 elsewhere).
+ * Products, differences and sums are fp64.  Rows need not be normalised.  A
+ * draft that is no word (negative, or vocab and above) is refused; a negative
+ * or NaN probability weighs nothing; next is -1 where the row's sum is not
+ * positive and finite, and always a word with a weight where it is.
+ *
+ *   target      device [n_draft + n_seq][vocab] of `type` (ENGRAM_F32, BF16 or
+ *               F16), rows target_stride elements apart, aligned as its elements.
+ *   draft_probs device [n_draft][vocab] of `type`, rows draft_stride apart.
+ *   draft       device int32 [n_draft]; uniform fp32 [n_draft]; last_uniform
+ *               fp32 [n_seq].
+ *   cu_draft    device int32 [n_seq + 1], ascending from 0 to n_draft; other
+ *               values leave results unspecified, and nothing out of bounds is
+ *               read or written.
+ *   tokens      device int32 [n_draft + n_seq], n_accepted int32 [n_seq].
+ *   ws          device workspace of engram_verify_draft_workspace bytes
+ *               (host-only; 0 for small vocabularies), 256-byte aligned; holds
+ *               nothing between calls; one call at a time may use it.
+ *
+ * Results are the same on every call with the same arguments.  n_seq == 0 is a
+ * no-op.  Errors: EINVAL, ERANGE (n_seq > 2^20, n_draft or vocab > 2^30, n_seq *
+ * vocab / 4096 > 2^23: split the batch), EUNSUPPORTED (type), EWORKSPACE.
+ */
+typedef struct engram_verify_draft_desc {
+    const void* target;
+    const void* draft_probs;
+    const int32_t* draft;
+    const float* uniform;
+    const float* last_uniform;
+    const int32_t* cu_draft;
+    int32_t* tokens;
+    int32_t* n_accepted;
+    int64_t n_seq;
+    int64_t n_draft;
+    int64_t vocab;
+    int64_t target_stride;
+    int64_t draft_stride;
+    uint32_t type;
+    uint32_t reserved0;
+} engram_verify_draft_desc;
+
+int engram_verify_draft_workspace(const engram_verify_draft_desc* desc, size_t* bytes);
+int engram_verify_draft(const engram_verify_draft_desc* desc, void* ws, size_t ws_bytes, void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* engram_status_string(int status);
