@@ -12,18 +12,28 @@
 // often its page has grown.  For e4m3 a power of two costs nothing, as a code's
 // digits are the same in every octave; for int8 it is half a bit on average.
 //
-// Prompts: each row is read once and its codes are written once: HBM-bound.
-// Single tokens: launch-bound, and the page is touched only where its scale
-// grows.
+// Prompts: each row is read once and its codes are written once: HBM-bound.  A
+// prompt of 32,768 tokens (8 heads of 128, normed and turned, bf16) takes 48 us
+// on pages of 16, 4.2 TB/s, where a copy of 2 GiB reaches 4.8 to 4.9; 57 on
+// pages of 64, whose rows are read a second time, from L2, and turned a second
+// time.  Single tokens: launch-bound (64 of them 4.5 us, 4.2 of kernel), and
+// the page is touched only where its scale grows.
+//
+// The norm's factor is the last product: it commutes with the rotation, x * w has
+// no rounding (two 16-bit numbers), and the page's factor is a power of two.  So
+// an element has the roundings of its rotation and one more, and the row's
+// largest element times the factor is the largest of the stored row.
 //
 // Mapping: as in norm_rope.hip D/16 lanes hold a row of 16 elements each.
-//   * Chunks: a workgroup takes one page of one request and up to 16 (head,
-//     side) pairs of it, a pair to a wave in turn, so that the cosines of the
-//     page's tokens are made once for all its heads (by way of LDS).  A wave
-//     holds 64 rows of head_dim 64 or 128 (32 of 256) as they were read, finds
-//     their maximum, and turns and rounds them from the same registers; pages
-//     with more new rows are read twice.
-//   * Single tokens: a wave takes as many pairs of a token as it holds rows.
+//   * Chunks: a workgroup takes one page of one request and up to 16 heads of one
+//     side, a head to a wave in turn, so that the cosines of the page's tokens are
+//     made once for all its heads (by way of LDS).  Up to two steps of rows (16
+//     rows of head_dim 128) are held as they are turned, with the next head's on
+//     their way; of more rows the maximum is found first, and they are read and
+//     turned again (held in registers they took all of them: 114 us on pages of
+//     16, 86 on pages of 64).
+//   * Single tokens: a wave takes as many (head, side) pairs of a token as it
+//     holds rows.
 #include <algorithm>
 
 #include "head_rows.h"
@@ -31,6 +41,7 @@
 namespace engram {
 namespace {
 
+typedef uint16_t u16x2v __attribute__((ext_vector_type(2)));
 constexpr uint32_t kMagnitude = 0x7FFFFFFFu, kInfinite = 0x7F800000u;
 
 // The two kinds of codes.
@@ -116,6 +127,44 @@ __device__ __forceinline__ uint32_t largest16(const float* x) {
     return m;
 }
 
+// The lanes' exchange within a row of LPH, and over the wave, without LDS.
+template <int kControl>
+__device__ __forceinline__ uint32_t moved(uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kControl, 0xF, 0xF, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;  // of 16 lanes
+template <int LPH>
+__device__ __forceinline__ float row_sum(float x) {
+    const auto add = [&](uint32_t y) { x += __builtin_bit_cast(float, y); };
+    const auto bits = [&]() { return __builtin_bit_cast(uint32_t, x); };
+    add(moved<kXor1>(bits()));
+    add(moved<kXor2>(bits()));
+    if constexpr (LPH >= 8) add(moved<kMirror8>(bits()));
+    if constexpr (LPH >= 16) add(moved<kMirror16>(bits()));
+    return x;
+}
+template <int LPH>
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+    x = max(x, moved<kXor1>(x));
+    x = max(x, moved<kXor2>(x));
+    if constexpr (LPH >= 8) x = max(x, moved<kMirror8>(x));
+    if constexpr (LPH >= 16) x = max(x, moved<kMirror16>(x));
+    return x;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    x = row_max<16>(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = max(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return max(static_cast<uint32_t>(b[0]), static_cast<uint32_t>(b[1]));
+}
+
+// 1 / sqrt(x) within an fp32 step; the instruction by itself knows no numbers below 2^-126.
+__device__ __forceinline__ float inverse_root(float x) {
+    const bool small = x < 0x1p-96f;
+    return __builtin_amdgcn_rsqf(small ? x * 0x1p96f : x) * (small ? 0x1p48f : 1.0f);
+}
+
 // A request's new tokens and the keys that they are.  Lengths are bounded by what exists.
 struct Fresh {
     uint32_t q0, q_len;
@@ -146,15 +195,281 @@ __device__ __forceinline__ uint32_t pages_before(const AppendPagesArgs& A, uint3
     return (static_cast<uint32_t>(min(max(A.cu_q[b], 0), n)) >> A.cache.page_shift) + 2u * b;
 }
 
+constexpr uint32_t kSteps = 8;   // of a wave's rows, whose cosines are held
+constexpr uint32_t kHeads = 16;  // of a workgroup at most, their keys or their values (append_heads)
+
+// One page of one request: rows row0 .. row0 + n_rows - 1 of it are new, tokens tok0 on.
 template <class T, int D, class C>
-__global__ __launch_bounds__(256) void append_pages_kernel(const AppendPagesArgs A) {
-    constexpr int LPH = D / 16;
-    constexpr uint32_t RPW = 64 / LPH, kSteps = D == 64 ? 4 : 8, kHold = kSteps * RPW;  // rows of a step, steps, rows held
-    constexpr uint32_t kPairs = 16;  // (head, side) pairs of a workgroup
-    __shared__ f32x2v sm_cs[kHold * (D / 2)];
-    __shared__ uint32_t sm_most[kPairs];
-    const uint32_t tid = threadIdx.x, lane = tid & 63u, j = lane & (LPH - 1u), of_step = lane / LPH;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+struct Page {
+    static constexpr int LPH = D / 16;
+    static constexpr uint32_t RPW = 64 / LPH, kHold = kSteps * RPW;  // rows of a step, rows whose cosines are held
+    const AppendPagesArgs& A;
+    f32x2v* cs;  // LDS: cosines and sines of kHold rows
+    float* fs;   // LDS: the norm's factors of kHold rows of each wave
+    int64_t page;
+    uint32_t row0, n_rows, tok0, head0, n_heads;
+    uint32_t wave, lane, j, of_step, rb;
+    Blocks bl;
+    float weight[16];
+
+    // A head's keys or values.
+    template <bool kKey>
+    struct Pair {
+        uint32_t head;
+    };
+    template <bool kKey>
+    __device__ __forceinline__ float* scale_of(Pair<kKey> p) const {
+        return (kKey ? A.cache.k_scale : A.cache.v_scale) + page * A.cache.n_kv_heads + p.head;
+    }
+    template <bool kKey>
+    __device__ __forceinline__ uint8_t* codes_of(Pair<kKey> p) const {
+        return (kKey ? A.cache.k + page * A.cache.k_page_stride : A.cache.v + page * A.cache.v_page_stride) +
+               (static_cast<int64_t>(p.head) << A.cache.page_shift) * D;
+    }
+    // the page's scale, if it holds rows
+    template <bool kKey>
+    __device__ __forceinline__ float held_scale(Pair<kKey> p) const { return row0 ? *scale_of(p) : 0.0f; }
+
+    // Row r (and of_step more) of the pair, as it was given; past the last row, that one again.
+    struct Raw {
+        u32x4v w[2];
+    };
+    template <bool kKey>
+    __device__ __forceinline__ Raw load(Pair<kKey> p, uint32_t r) const {
+        constexpr int kSide = kKey ? 0 : 1;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(A.src[kSide]) + p.head * A.src_head[kSide] +
+                              (tok0 + min(r + of_step, n_rows - 1u)) * A.src_tok[kSide];
+        return Raw{{*reinterpret_cast<const u32x4v*>(src + bl.b0 * 8u), *reinterpret_cast<const u32x4v*>(src + bl.b1 * 8u)}};
+    }
+    // Where pair q of row r's cosine and sine lie: 16-byte blocks of two pairs, turned within their 64 bytes by the lane that
+    // reads them, so that 16 lanes of a read meet on no bank (all rows begin on the same one).
+    __device__ __forceinline__ uint32_t turn_at(uint32_t r, uint32_t q) const {
+        const uint32_t turn = (r * LPH + (q >> 3)) >> 2;
+        return r * (8u * rb) + (q & ~7u) + ((q + 2u * turn) & 6u) + (q & 1u);
+    }
+    __device__ __forceinline__ Turn turn_for(uint32_t r) const {
+        Turn t;
+#pragma unroll
+        for (uint32_t e = 0; e < 8; e += 2) {
+            const uint32_t q = A.interleaved ? (e < 4 ? 4u * j + e : 4u * (j + rb) + (e - 4)) : 8u * j + e;
+            const f32x4v x = *reinterpret_cast<const f32x4v*>(cs + turn_at(r, q));
+            t.c[e] = x[0];
+            t.s[e] = x[1];
+            t.c[e + 1] = x[2];
+            t.s[e + 1] = x[3];
+        }
+        return t;
+    }
+    // Cosines and sines of rows r0 .. r0 + kHold - 1, by the whole workgroup.
+    __device__ __forceinline__ void make_turns(uint32_t r0) const {
+        if (!rb) return;
+        const uint32_t pairs = 8u * rb, n = min(n_rows - r0, kHold) * pairs;
+        for (uint32_t i = threadIdx.x; i < n; i += 256u) {
+            const uint32_t row = i / pairs;
+            const uint32_t q = i - row * pairs;
+            cs[turn_at(row, q)] = cos_sin(static_cast<double>(A.positions[tok0 + r0 + row]) * A.inv_freq[q]);
+        }
+    }
+    // The row as it is to be stored but for the norm's factor, which commutes with the rotation and is left to the last
+    // product.  x * w has no rounding: 8 digits of each in bf16, 11 in fp16.
+    template <bool kKey>
+    __device__ __forceinline__ void turned(const Raw& h, Pair<kKey>, uint32_t r, uint32_t r0, float* x) const {
+        unpack8<T>(h.w[0], x);
+        unpack8<T>(h.w[1], x + 8);
+        if constexpr (kKey) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] *= weight[e];
+            if (j < rb) turn_row(x, turn_for(min(r + of_step, n_rows - 1u) - r0), A.interleaved != 0);
+        }
+    }
+    template <bool kKey>
+    __device__ __forceinline__ float factor(const Raw& h, Pair<kKey>) const {
+        if constexpr (!kKey) return 1.0f;
+        float x[16], ss = 0.0f;
+        unpack8<T>(h.w[0], x);
+        unpack8<T>(h.w[1], x + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
+        const float f = inverse_root(row_sum<LPH>(ss) * (1.0f / D) + A.eps);
+        return A.weight ? f : 1.0f;
+    }
+    // The largest magnitude of the row, by its bits.
+    static __device__ __forceinline__ uint32_t times(uint32_t magnitude, float f) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, magnitude) * f) & kMagnitude;
+    }
+    template <bool kKey>
+    __device__ __forceinline__ uint32_t largest(const Raw& h, Pair<kKey> p, uint32_t r, uint32_t r0, float f) const {
+        if constexpr (kKey) {
+            float x[16];
+            turned(h, p, r, r0, x);
+            return times(largest16(x), f);
+        } else {  // 16-bit magnitudes are in order as whole numbers
+            u16x2v m = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2v, h.w[i / 4][i % 4] & 0x7FFF7FFFu));
+            const uint32_t both = max(static_cast<uint32_t>(m[0]), static_cast<uint32_t>(m[1]));
+            return __builtin_bit_cast(uint32_t, T::lo(both));
+        }
+    }
+    // The page's scale, and the codes that it holds; the new rows' factor.
+    template <bool kKey>
+    __device__ __forceinline__ float settle(Pair<kKey> p, uint32_t most, float old) const {
+        const Scale s = grown(scale_for<C>(most), old, row0 > 0u);
+        if (lane == 0) *scale_of(p) = s.now;
+        if (s.ratio != 1.0f) {
+            uint8_t* const codes = codes_of(p);
+            for (uint32_t i = lane * 16u; i < row0 * D; i += 1024u) {
+                u32x4v* const q = reinterpret_cast<u32x4v*>(codes + i);
+                *q = again<C>(*q, s.ratio);
+            }
+        }
+        return s.by;
+    }
+    template <bool kKey>
+    __device__ __forceinline__ void store(const Raw& h, Pair<kKey> p, uint32_t r, uint32_t r0, float by) const {
+        float x[16];
+        turned(h, p, r, r0, x);
+        put(x, p, r, by);
+    }
+    template <bool kKey>
+    __device__ __forceinline__ void put(const float* x, Pair<kKey> p, uint32_t r, float by) const {
+        if (r + of_step < n_rows) encode16<C>(codes_of(p) + static_cast<uint64_t>(row0 + r + of_step) * D, x, by, bl);
+    }
+
+    // Up to two steps of rows: held as they are turned, the next head's on their way.
+    template <bool kKey>
+    __device__ __forceinline__ void few_rows() const {
+        const auto ask = [&](uint32_t k, Raw* raw) {
+            const Pair<kKey> p = {head0 + min(k, n_heads - 1u)};
+            raw[0] = load(p, 0);
+            raw[1] = load(p, RPW);
+            return held_scale(p);
+        };
+        Raw next[2];
+        float next_old = ask(wave, next);
+        if (kKey) {
+            make_turns(0);
+            __syncthreads();
+        }
+        for (uint32_t k = wave; k < n_heads; k += 4u) {
+            const Pair<kKey> p = {head0 + k};
+            float x[2][16], f[2];
+            uint32_t m = 0;
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i) {
+                f[i] = factor(next[i], p);
+                turned(next[i], p, i * RPW, 0, x[i]);
+                m = max(m, times(largest16(x[i]), f[i]));
+            }
+            const float old = next_old;
+            if (k + 4u < n_heads) next_old = ask(k + 4u, next);
+            const float by = settle(p, wave_max(m), old);
+            put(x[0], p, 0, f[0] * by);
+            if (RPW < n_rows) put(x[1], p, RPW, f[1] * by);
+        }
+    }
+
+    // More: read twice, the second time from the caches.
+    template <bool kKey>
+    __device__ __forceinline__ void more_rows() const {
+        if (kKey) {
+            make_turns(0);
+            __syncthreads();
+        }
+        for (uint32_t k = wave; k < n_heads; k += 4u) {
+            const Pair<kKey> p = {head0 + k};
+            const float old = held_scale(p);
+            const float by = settle(p, wave_max(largest_of(p, 0, n_rows)), old);
+            store_all(p, 0, n_rows, by, true);
+        }
+    }
+    template <bool kKey>
+    __device__ __forceinline__ uint32_t largest_of(Pair<kKey> p, uint32_t r0, uint32_t r1) const {
+        uint32_t m = 0;
+        float* const mine = fs + wave * kHold + of_step;  // a row's lanes all write its factor, and each reads its own word
+        each(p, r0, r1, [&](const Raw& raw, uint32_t r) {
+            const float f = factor(raw, p);
+            if (kKey && r - r0 < kHold) mine[r - r0] = f;
+            m = max(m, largest(raw, p, r, r0, f));
+        });
+        return m;
+    }
+    template <bool kKey>
+    __device__ __forceinline__ void store_all(Pair<kKey> p, uint32_t r0, uint32_t r1, float by, bool known) const {
+        const float* const mine = fs + wave * kHold + of_step;
+        each(p, r0, r1, [&](const Raw& raw, uint32_t r) {
+            const float f = !kKey ? 1.0f : known && r - r0 < kHold ? mine[r - r0] : factor(raw, p);
+            store(raw, p, r, r0, f * by);
+        });
+    }
+    // A head's rows step by step, kAhead steps on their way.
+    template <bool kKey, class F>
+    __device__ __forceinline__ void each(Pair<kKey> p, uint32_t r0, uint32_t r1, F f) const {
+        constexpr uint32_t kAhead = 2;
+        Raw raw[kAhead];
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i) raw[i] = load(p, r0 + i * RPW);
+        for (uint32_t r = r0; r < r1; r += kAhead * RPW) {
+#pragma unroll
+            for (uint32_t i = 0; i < kAhead; ++i) {
+                const Raw now = raw[i];
+                raw[i] = load(p, r + (kAhead + i) * RPW);
+                if (i == 0 || r + i * RPW < r1) f(now, r + i * RPW);
+            }
+        }
+    }
+
+    // More rows than a wave holds: read twice.  most: LDS of kHeads words.
+    template <bool kKey>
+    __device__ __forceinline__ void in_parts(uint32_t* most) const {
+        if (threadIdx.x < kHeads) most[threadIdx.x] = 0;
+        for (uint32_t pass = 0; pass < 2; ++pass) {
+            for (uint32_t r0 = 0; r0 < n_rows; r0 += kHold) {
+                __syncthreads();
+                if (kKey) make_turns(r0);
+                __syncthreads();
+                for (uint32_t k = wave; k < n_heads; k += 4u) {
+                    const Pair<kKey> p = {head0 + k};
+                    const uint32_t r1 = min(r0 + kHold, n_rows);
+                    if (pass == 0) {
+                        const uint32_t m = wave_max(largest_of(p, r0, r1));
+                        if (lane == 0) most[k] = max(most[k], m);  // the wave's own
+                    } else {
+                        store_all(p, r0, r1, __builtin_bit_cast(float, most[k]), false);
+                    }
+                }
+            }
+            if (pass == 0) {
+                __syncthreads();
+                for (uint32_t k = wave; k < n_heads; k += 4u) {
+                    const Pair<kKey> p = {head0 + k};
+                    const float by = settle(p, most[k], held_scale(p));
+                    if (lane == 0) most[k] = __builtin_bit_cast(uint32_t, by);
+                }
+            }
+        }
+    }
+
+    template <bool kKey>
+    __device__ __forceinline__ void append(uint32_t* most) const {
+        if (n_rows <= 2 * RPW)
+            few_rows<kKey>();
+        else if (n_rows <= kHold || !kKey || !rb)
+            more_rows<kKey>();
+        else
+            in_parts<kKey>(most);
+    }
+};
+
+template <class T, int D, class C>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void append_pages_kernel(const AppendPagesArgs A,
+                                                                                                           uint32_t heads_each) {
+    using P = Page<T, D, C>;
+    __shared__ __attribute__((aligned(16))) f32x2v sm_cs[P::kHold * (D / 2)];
+    __shared__ float sm_fs[4 * P::kHold];
+    __shared__ uint32_t sm_most[kHeads];
+    const uint32_t lane = threadIdx.x & 63u;
     uint32_t b, at;  // request, and which of its pages
     if (A.pages_per) {
         b = blockIdx.x / A.pages_per;
@@ -180,140 +495,32 @@ __global__ __launch_bounds__(256) void append_pages_kernel(const AppendPagesArgs
     if (in_table > static_cast<uint32_t>(req.kv_len - 1) >> shift) return;
     const int64_t page = A.table[b * A.table_stride + in_table];
     if (page < 0 || page >= A.cache.n_pages) return;
-    // rows row0 .. row0 + n_rows - 1 of the page are new; in_table <= 2^31 / page, so that its keys are int32 but for the end
     const uint32_t key0 = in_table << shift;
-    const uint32_t row0 = max(static_cast<uint32_t>(lo), key0) - key0;
-    const uint32_t n_rows = min(static_cast<uint32_t>(req.kv_len) - key0, 1u << shift) - row0;
-    const uint32_t tok0 = req.q0 + (key0 + row0 - static_cast<uint32_t>(req.first));
-
-    const uint32_t rb = A.rotary / 16u, heads = A.cache.n_kv_heads;
-    const uint32_t pair0 = blockIdx.y * kPairs, n_pairs = min(2u * heads - pair0, kPairs);
-    const bool il = A.interleaved != 0, turns = j < rb, any_key = pair0 < heads;
-    const Blocks bl = blocks_of(j, rb);
-    float weight[16];
-    if (A.weight && any_key) {
-        const uint16_t* wp = reinterpret_cast<const uint16_t*>(A.weight);
-        unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + bl.b0 * 8u), weight);
-        unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + bl.b1 * 8u), weight + 8);
-    }
-    struct Held {
-        u32x4v w[kSteps][2];
-    };
-    const auto load = [&](uint32_t pair, uint32_t r0) {
-        Held h;
-        const uint32_t side = pair < heads ? 0u : 1u, head = side ? pair - heads : pair;
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(side ? A.src[1] : A.src[0]) +
-                              head * (side ? A.src_head[1] : A.src_head[0]);
-        const int64_t stride = side ? A.src_tok[1] : A.src_tok[0];
+    P p = {A, sm_cs, sm_fs};
+    p.page = page;
+    p.row0 = max(static_cast<uint32_t>(lo), key0) - key0;
+    p.n_rows = min(static_cast<uint32_t>(req.kv_len) - key0, 1u << shift) - p.row0;
+    p.tok0 = req.q0 + (key0 + p.row0 - static_cast<uint32_t>(req.first));
+    const uint32_t of_side = gridDim.y / 2u, part = blockIdx.y % of_side;
+    p.head0 = part * heads_each;
+    p.n_heads = min(A.cache.n_kv_heads - p.head0, heads_each);
+    p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    p.lane = lane;
+    p.j = lane & (P::LPH - 1u);
+    p.of_step = lane / P::LPH;
+    p.rb = A.rotary / 16u;
+    p.bl = blocks_of(p.j, p.rb);
+    if (blockIdx.y < of_side) {
 #pragma unroll
-        for (uint32_t s = 0; s < kSteps; ++s) {
-            if (r0 + s * RPW < n_rows) {  // the last row again, where a step is not full
-                const uint16_t* p = src + (tok0 + min(r0 + s * RPW + of_step, n_rows - 1u)) * stride;
-                h.w[s][0] = *reinterpret_cast<const u32x4v*>(p + bl.b0 * 8u);
-                h.w[s][1] = *reinterpret_cast<const u32x4v*>(p + bl.b1 * 8u);
-            }
+        for (int e = 0; e < 16; ++e) p.weight[e] = 1.0f;
+        if (A.weight) {
+            const uint16_t* wp = reinterpret_cast<const uint16_t*>(A.weight);
+            unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + p.bl.b0 * 8u), p.weight);
+            unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + p.bl.b1 * 8u), p.weight + 8);
         }
-        return h;
-    };
-    // the row of step s as it is to be stored
-    const auto row_of = [&](const Held& h, uint32_t pair, uint32_t s, uint32_t r0, float* x) __attribute__((always_inline)) {
-        unpack8<T>(h.w[s][0], x);
-        unpack8<T>(h.w[s][1], x + 8);
-        if (pair < heads) {
-            if (A.weight) norm_row<LPH>(x, weight, A.eps);
-            const uint32_t row = min(s * RPW + of_step, n_rows - 1u - r0);  // as it was loaded
-            if (turns) turn_row(x, turn_of(sm_cs + row * (8u * rb), j, rb, il), il);
-        }
-    };
-    const auto make_turns = [&](uint32_t r0) {
-        if (!rb || !any_key) return;
-        const uint32_t pairs = 8u * rb, n = min(n_rows - r0, kHold) * pairs;
-        for (uint32_t i = tid; i < n; i += 256u) {
-            const uint32_t row = i / pairs;
-            sm_cs[i] = cos_sin(static_cast<double>(A.positions[tok0 + r0 + row]) * A.inv_freq[i - row * pairs]);
-        }
-    };
-    const auto largest = [&](const Held& h, uint32_t pair, uint32_t r0) {
-        uint32_t m = 0;
-#pragma unroll
-        for (uint32_t s = 0; s < kSteps; ++s) {
-            if (r0 + s * RPW < n_rows) {
-                float x[16];
-                row_of(h, pair, s, r0, x);
-                m = max(m, largest16(x));
-            }
-        }
-        return m;
-    };
-    const auto finish = [&](uint32_t m) {
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), k)));
-        return m;
-    };
-    // the page's scale and the codes that it holds
-    const auto settle = [&](uint32_t pair, uint32_t m, float old) {
-        const uint32_t side = pair < heads ? 0u : 1u, head = side ? pair - heads : pair;
-        const Scale s = grown(scale_for<C>(m), old, row0 > 0u);
-        if (lane == 0) (side ? A.cache.v_scale : A.cache.k_scale)[page * heads + head] = s.now;
-        if (s.ratio != 1.0f) {
-            uint8_t* const codes = (side ? A.cache.v + page * A.cache.v_page_stride : A.cache.k + page * A.cache.k_page_stride) +
-                                   (static_cast<int64_t>(head) << shift) * D;
-            for (uint32_t i = lane * 16u; i < row0 * D; i += 1024u) {
-                u32x4v* const p = reinterpret_cast<u32x4v*>(codes + i);
-                *p = again<C>(*p, s.ratio);
-            }
-        }
-        return s.by;
-    };
-    const auto old_scale = [&](uint32_t pair) {
-        return row0 ? (pair < heads ? A.cache.k_scale : A.cache.v_scale)[page * heads + (pair < heads ? pair : pair - heads)] : 0.0f;
-    };
-    const auto store = [&](const Held& h, uint32_t pair, uint32_t r0, float by) {
-        const uint32_t side = pair < heads ? 0u : 1u, head = side ? pair - heads : pair;
-        uint8_t* const codes = (side ? A.cache.v + page * A.cache.v_page_stride : A.cache.k + page * A.cache.k_page_stride) +
-                               ((static_cast<int64_t>(head) << shift) + row0) * D;
-#pragma unroll
-        for (uint32_t s = 0; s < kSteps; ++s) {
-            const uint32_t r = r0 + s * RPW + of_step;
-            if (r0 + s * RPW < n_rows) {
-                float x[16];
-                row_of(h, pair, s, r0, x);
-                if (r < n_rows) encode16<C>(codes + static_cast<uint64_t>(r) * D, x, by, bl);
-            }
-        }
-    };
-    if (n_rows <= kHold) {
-        make_turns(0);
-        __syncthreads();
-        for (uint32_t k = wave; k < n_pairs; k += 4u) {
-            const uint32_t pair = pair0 + k;
-            const float old = old_scale(pair);
-            const Held h = load(pair, 0);
-            store(h, pair, 0, settle(pair, finish(largest(h, pair, 0)), old));
-        }
-        return;
-    }
-    if (tid < kPairs) sm_most[tid] = 0;
-    for (uint32_t r0 = 0; r0 < n_rows; r0 += kHold) {
-        __syncthreads();
-        make_turns(r0);
-        __syncthreads();
-        for (uint32_t k = wave; k < n_pairs; k += 4u) {
-            const uint32_t m = finish(largest(load(pair0 + k, r0), pair0 + k, r0));
-            if (lane == 0) sm_most[k] = max(sm_most[k], m);  // the wave's own
-        }
-    }
-    __syncthreads();
-    for (uint32_t k = wave; k < n_pairs; k += 4u) {
-        const float by = settle(pair0 + k, sm_most[k], old_scale(pair0 + k));
-        if (lane == 0) sm_most[k] = __builtin_bit_cast(uint32_t, by);
-    }
-    for (uint32_t r0 = 0; r0 < n_rows; r0 += kHold) {
-        __syncthreads();
-        make_turns(r0);
-        __syncthreads();
-        for (uint32_t k = wave; k < n_pairs; k += 4u)
-            store(load(pair0 + k, r0), pair0 + k, r0, __builtin_bit_cast(float, sm_most[k]));
+        p.template append<true>(sm_most);
+    } else {
+        p.template append<false>(sm_most);
     }
 }
 
@@ -360,25 +567,28 @@ __global__ __launch_bounds__(256) void append_token_kernel(const AppendPagesArgs
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-    float x[16];
+    float x[16], f = 1.0f;
     unpack8<T>(raw[0], x);
     unpack8<T>(raw[1], x + 8);
-    if (side == 0) {  // the same for all lanes of a row
+    if (side == 0) {  // the same for all lanes of a row; the norm's factor comes last, as above
         if (A.weight) {
-            float w[16];
+            float w[16], ss = 0.0f;
             const uint16_t* wp = reinterpret_cast<const uint16_t*>(A.weight);
             unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + bl.b0 * 8u), w);
             unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + bl.b1 * 8u), w + 8);
-            norm_row<LPH>(x, w, A.eps);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                ss = __builtin_fmaf(x[e], x[e], ss);
+                x[e] *= w[e];
+            }
+            f = inverse_root(row_sum<LPH>(ss) * (1.0f / D) + A.eps);
         }
         if (j < rb) turn_row(x, turn_of(sm_cs[wave], j, rb, il), il);
     }
-    uint32_t m = largest16(x);
-#pragma unroll
-    for (int k = 1; k < LPH; k <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), k)));
+    const uint32_t m = row_max<LPH>(__builtin_bit_cast(uint32_t, __builtin_bit_cast(float, largest16(x)) * f) & kMagnitude);
     if (!live) return;
     const Scale s = grown(scale_for<C>(m), old, place > 0u);
-    encode16<C>(codes + static_cast<uint64_t>(place) * D, x, s.by, bl);
+    encode16<C>(codes + static_cast<uint64_t>(place) * D, x, f * s.by, bl);
     if (j == 0) *scale = s.now;
     if (s.ratio != 1.0f) {
 #pragma unroll 4
@@ -398,7 +608,10 @@ hipError_t pages_one(const AppendPagesArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((append_token_kernel<T, D, C>), dim3((a.n_seq * steps + 3u) / 4u), dim3(256), 0, stream, a, steps);
     } else {
         const uint32_t pages = a.pages_per ? a.n_seq * a.pages_per : (a.n_tok >> a.cache.page_shift) + 2u * a.n_seq;
-        hipLaunchKernelGGL((append_pages_kernel<T, D, C>), dim3(pages, (pairs + 15u) / 16u), dim3(256), 0, stream, a);
+        const uint32_t heads = a.cache.n_kv_heads;
+        const uint32_t each = append_heads(pages, heads);
+        hipLaunchKernelGGL((append_pages_kernel<T, D, C>), dim3(pages, 2u * ((heads + each - 1u) / each)), dim3(256), 0, stream, a,
+                           each);
     }
     return hipGetLastError();
 }

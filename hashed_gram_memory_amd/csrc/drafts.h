@@ -28,8 +28,8 @@ struct TablesArgs {
     uint32_t page_shift;
 };
 
-// Whether one workgroup does it all, without a workspace: a request to a thread, and up to eight tokens.  (On one card 64
-// requests of 6 tokens take a kernel of 5.7 us so and two of 9.7 together; 1,024 of 8 tokens are as quick in either form.)
+// Whether one workgroup does it all, without a workspace: a request to a thread, and up to eight tokens.  (64 requests of 6
+// tokens take 5.9 us so and 9.0 in two launches, 1,024 of 8 tokens 11.9 and 11.3, 512 of 16 10.0 and 9.7.)
 constexpr uint32_t kOneRequests = 1024, kOneTokens = 8192;
 inline bool tables_in_one(uint64_t n_seq, uint64_t n_tok) { return n_seq <= kOneRequests && n_tok <= kOneTokens; }
 inline size_t tables_workspace(uint64_t n_seq, uint64_t n_tok) {

@@ -134,20 +134,38 @@ __device__ __forceinline__ void deal(const TablesArgs& A, const Sums& s, uint32_
     }
 }
 
-__device__ __forceinline__ void place_token(const TablesArgs& A, const Sums& s, uint32_t t) {
-    int64_t slot = -1;
-    uint32_t pos = 0;
-    if (A.n_seq && t < s.cu[A.n_seq]) {
-        const uint32_t b = find(s.cu, A.n_seq, t), keys = s.keys[b];
-        if (keys) {
-            pos = keys - (s.cu[b + 1] - t);
-            const uint32_t j = pos >> A.page_shift, before = s.before[b];
-            const int32_t page = j < before ? A.table[b * A.table_stride + j] : from_pool(A, s, s.taken[b] + (j - before));
-            slot = (static_cast<int64_t>(page) << A.page_shift) + (pos & ((1u << A.page_shift) - 1u));
+// kRun neighbouring tokens from t on: their request is looked for once, and then followed.
+constexpr uint32_t kRun = 4;
+__device__ __forceinline__ void place_tokens(const TablesArgs& A, const Sums& s, uint32_t t) {
+    const uint32_t end = A.n_seq ? s.cu[A.n_seq] : 0u;
+    uint32_t b = 0, b_end = 0, keys = 0, before = 0, taken = 0;
+    if (t < end) b = find(s.cu, A.n_seq, t);
+#pragma unroll
+    for (uint32_t i = 0; i < kRun; ++i, ++t) {
+        if (t >= A.n_tok) return;
+        int64_t slot = -1;
+        uint32_t pos = 0;
+        if (t < end) {
+            if (t >= b_end) {
+                if (i) {
+                    do ++b;
+                    while (s.cu[b + 1] <= t);
+                }
+                b_end = s.cu[b + 1];
+                keys = s.keys[b];
+                before = s.before[b];
+                taken = s.taken[b];
+            }
+            if (keys) {
+                pos = keys - (b_end - t);
+                const uint32_t j = pos >> A.page_shift;
+                const int32_t page = j < before ? A.table[b * A.table_stride + j] : from_pool(A, s, taken + (j - before));
+                slot = (static_cast<int64_t>(page) << A.page_shift) + (pos & ((1u << A.page_shift) - 1u));
+            }
         }
+        A.slots[t] = slot;
+        A.positions[t] = static_cast<int32_t>(pos);
     }
-    A.slots[t] = slot;
-    A.positions[t] = static_cast<int32_t>(pos);
 }
 
 template <bool kOne>
@@ -248,12 +266,12 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(const TablesArgs A) {
     if constexpr (kOne) {
         __syncthreads();
         const Sums s = {sm_cu, sm_taken, sm_back, sm_before, sm_keys, sm_taken_all, backs.all, n_free};
-        for (uint32_t t = tid; t < A.n_tok; t += kThreads) place_token(A, s, t);
+        for (uint32_t t = tid * kRun; t < A.n_tok; t += kThreads * kRun) place_tokens(A, s, t);
         for (uint32_t k = tid; k < max(s.n_taken, s.n_back); k += kThreads) deal(A, s, k);
     }
 }
 
-constexpr uint32_t kSpreadThreads = 256, kSpreadTokens = 1024;  // of a workgroup
+constexpr uint32_t kSpreadThreads = 256, kSpreadTokens = kSpreadThreads * kRun;  // of a workgroup
 constexpr uint32_t kStaged = 4096;  // requests whose offsets lie in LDS
 
 __global__ __launch_bounds__(kSpreadThreads) void spread_kernel(const TablesArgs A, uint32_t token_groups) {
@@ -268,11 +286,7 @@ __global__ __launch_bounds__(kSpreadThreads) void spread_kernel(const TablesArgs
             __syncthreads();
             s.cu = sm_cu;
         }
-#pragma unroll
-        for (uint32_t i = 0; i < kSpreadTokens / kSpreadThreads; ++i) {
-            const uint32_t t = blockIdx.x * kSpreadTokens + i * kSpreadThreads + threadIdx.x;
-            if (t < A.n_tok) place_token(A, s, t);
-        }
+        place_tokens(A, s, (blockIdx.x * kSpreadThreads + threadIdx.x) * kRun);
     } else {
         const uint32_t step = (gridDim.x - token_groups) * kSpreadThreads;
         for (uint32_t k = (blockIdx.x - token_groups) * kSpreadThreads + threadIdx.x; k < max(s.n_taken, s.n_back); k += step)

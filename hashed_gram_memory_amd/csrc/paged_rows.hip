@@ -284,7 +284,7 @@ __global__ __launch_bounds__(kWaves * 64)
         Words<16> kw[2][ES == 1 ? CH / 2 : CH];  // keys base + n and base + 16 + n
         Words<EPL * ES> vw[2][4];                // keys base + 4g + 0..3 and base + 16 + 4g + 0..3, which are also this lane's scores
         f32x4v ks[2], vs[2];
-        float kp[4], vp[4];  // scales of the pages of a step's runs of 8 keys
+        float kp[2], vp[2];  // the same of pages with one scale, of this lane's runs of 8 keys
         auto ask_k = [&](int32_t base, const Pages& pg) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -295,9 +295,8 @@ __global__ __launch_bounds__(kWaves * 64)
                 for (uint32_t i = 0; i < (ES == 1 ? CH / 2 : CH); ++i)
                     kw[t][i] = load_words<16>(p + (ES == 1 ? 64 * i + 16 * g : (32 * i + 8 * g) * 2));
                 if constexpr (kPages) {
-#pragma unroll
-                    for (int i = 2 * t; i < 2 * t + 2; ++i)
-                        kp[i] = load_scalar(A.cache.k_scale + (static_cast<int64_t>(max(pg.p[i], 0)) * heads + h));
+                    const int64_t c = max(pg.p[2 * t], 0), d = max(pg.p[2 * t + 1], 0);
+                    kp[t] = A.cache.k_scale[(g >> 1 ? d : c) * heads + h];
                 } else if constexpr (kE4m3) {
                     const int64_t c = max(pg.p[2 * t], 0), d = max(pg.p[2 * t + 1], 0);
                     const uint32_t at = (static_cast<uint32_t>(base) + 16 * t + 4u * g) & in_page;
@@ -314,9 +313,8 @@ __global__ __launch_bounds__(kWaves * 64)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) vw[t][i] = load_words<EPL * ES>(p + i * D * ES);
                 if constexpr (kPages) {
-#pragma unroll
-                    for (int i = 2 * t; i < 2 * t + 2; ++i)
-                        vp[i] = load_scalar(A.cache.v_scale + (static_cast<int64_t>(max(pg.p[i], 0)) * heads + h));
+                    const int64_t c = max(pg.p[2 * t], 0), d = max(pg.p[2 * t + 1], 0);
+                    vp[t] = A.cache.v_scale[(g >> 1 ? d : c) * heads + h];
                 } else if constexpr (kE4m3) {
                     const int64_t c = max(pg.p[2 * t], 0), d = max(pg.p[2 * t + 1], 0);
                     vs[t] = *reinterpret_cast<const f32x4v*>(A.cache.v_scale + ((((g >> 1 ? d : c) * heads) << shift) + of_head + key));
@@ -360,9 +358,9 @@ __global__ __launch_bounds__(kWaves * 64)
                     for (uint32_t c = 0; c < CH; ++c) {
                         u32x4v a;
                         if constexpr (kE4m3) {
-                            const uint32_t w0 = kw[t][c / 2].w[2 * (c % 2)], w1 = kw[t][c / 2].w[2 * (c % 2) + 1];
-                            a = u32x4v{from_codes<T, kHeld, false>(w0), from_codes<T, kHeld, true>(w0),
-                                       from_codes<T, kHeld, false>(w1), from_codes<T, kHeld, true>(w1)};
+                            const u32x2v w0 = from_codes<T, kHeld>(kw[t][c / 2].w[2 * (c % 2)]);
+                            const u32x2v w1 = from_codes<T, kHeld>(kw[t][c / 2].w[2 * (c % 2) + 1]);
+                            a = u32x4v{w0[0], w0[1], w1[0], w1[1]};
                         } else {
                             a = u32x4v{kw[t][c].w[0], kw[t][c].w[1], kw[t][c].w[2], kw[t][c].w[3]};
                         }
@@ -372,11 +370,7 @@ __global__ __launch_bounds__(kWaves * 64)
                 float x[2][4];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    float by = A.scale_log2;
-                    if constexpr (kPages) {
-                        const float a = kp[2 * t], b = kp[2 * t + 1];
-                        by *= g >> 1 ? b : a;
-                    }
+                    const float by = kPages ? A.scale_log2 * kp[t] : A.scale_log2;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         x[t][i] = s[t][i] * by;
@@ -420,17 +414,12 @@ __global__ __launch_bounds__(kWaves * 64)
                 float p[2][4];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    float vs_page = 0.0f;
-                    if constexpr (kPages) {
-                        const float a = vp[2 * t], b = vp[2 * t + 1];
-                        vs_page = g >> 1 ? b : a;
-                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         p[t][i] = __builtin_amdgcn_exp2f(x[t][i] + nb);
                         l += p[t][i];
                         if constexpr (kE4m3)
-                            p[t][i] = (seen >> (16 * t + i)) & 1u ? p[t][i] * (kPages ? vs_page : vs[t][i]) : 0.0f;
+                            p[t][i] = (seen >> (16 * t + i)) & 1u ? p[t][i] * (kPages ? vp[t] : vs[t][i]) : 0.0f;
                     }
                 }
 
@@ -443,9 +432,11 @@ __global__ __launch_bounds__(kWaves * 64)
                     for (int i = 0; i < 4; ++i) {
                         if constexpr (kE4m3) {
 #pragma unroll
-                            for (int e = 0; e < EPL / 2; ++e)
-                                v[4 * t + i].w[e] = (e & 1) ? from_codes<P, kHeld, true>(vw[t][i].w[e / 2])
-                                                            : from_codes<P, kHeld, false>(vw[t][i].w[e / 2]);
+                            for (int e = 0; e < EPL / 4; ++e) {
+                                const u32x2v w = from_codes<P, kHeld>(vw[t][i].w[e]);
+                                v[4 * t + i].w[2 * e] = w[0];
+                                v[4 * t + i].w[2 * e + 1] = w[1];
+                            }
                         } else {
                             v[4 * t + i] = vw[t][i];
                         }

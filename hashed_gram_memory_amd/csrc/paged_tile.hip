@@ -128,8 +128,8 @@ __device__ __forceinline__ void wait_loads() {
 // eight codes as 16-bit numbers
 template <class T, int kHeld>
 __device__ __forceinline__ u32x4v widen(u32x2v w) {
-    return u32x4v{from_codes<T, kHeld, false>(w[0]), from_codes<T, kHeld, true>(w[0]), from_codes<T, kHeld, false>(w[1]),
-                  from_codes<T, kHeld, true>(w[1])};
+    const u32x2v a = from_codes<T, kHeld>(w[0]), b = from_codes<T, kHeld>(w[1]);
+    return u32x4v{a[0], a[1], b[0], b[1]};
 }
 
 template <class T, int D, int kHeld, int kWaves>

@@ -64,12 +64,17 @@ struct Bf16 : Halves<0x7F80u, 0x3F80u> {
     static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, kHigh));
     }
-    // two int8 codes likewise: their floats have no digits below this type's
-    template <bool kHigh>
-    static __device__ __forceinline__ uint32_t from_i8(uint32_t w) {
-        const float a = static_cast<float>(static_cast<int8_t>(w >> (kHigh ? 16 : 0)));
-        const float b = static_cast<float>(static_cast<int8_t>(w >> (kHigh ? 24 : 8)));
-        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+    // four int8 codes likewise: their floats have no digits below this type's.  (The compiler takes a byte out of its word
+    // first, and 3.25 instructions to a code where these are 1.5.)
+    static __device__ __forceinline__ u32x2v from_i8(uint32_t w) {
+        uint32_t a, b, c, d;
+        asm("v_cvt_f32_i32_sdwa %0, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0\n\t"
+            "v_cvt_f32_i32_sdwa %1, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1\n\t"
+            "v_cvt_f32_i32_sdwa %2, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2\n\t"
+            "v_cvt_f32_i32_sdwa %3, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
+            : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+            : "v"(w));
+        return u32x2v{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
     }
     // Softmax terms are held as 2^kShift at their row's reference, and may pass
     // it by 2^kSlack before the reference moves.
@@ -100,11 +105,12 @@ struct F16 : Halves<0x7C00u, 0x3C00u> {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, kHigh));
     }
     // 1,024 + 128 + the code by its bits, less 1,152: both exact
-    template <bool kHigh>
-    static __device__ __forceinline__ uint32_t from_i8(uint32_t w) {
-        const uint32_t x = __builtin_amdgcn_perm(w ^ 0x80808080u, 0x64646464u, kHigh ? 0x00070006u : 0x00050004u);
+    static __device__ __forceinline__ u32x2v from_i8(uint32_t w) {
         const f16x2v off = {static_cast<_Float16>(1152.0f), static_cast<_Float16>(1152.0f)};
-        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2v, x) - off);
+        const uint32_t u = w ^ 0x80808080u;
+        const f16x2v a = __builtin_bit_cast(f16x2v, __builtin_amdgcn_perm(u, 0x64646464u, 0x00050004u)) - off;
+        const f16x2v b = __builtin_bit_cast(f16x2v, __builtin_amdgcn_perm(u, 0x64646464u, 0x00070006u)) - off;
+        return u32x2v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
     }
     // fp16 ends at 65,504 and has all its digits down to 2^-14: with a term of
     // 2^14 at most, one of 2^-21 of the reference is still a normal number.
@@ -115,13 +121,13 @@ struct F16 : Halves<0x7C00u, 0x3C00u> {
 // or for each page and head (e4m3, int8).
 enum Held : int { kHalves, kE4m3Rows, kE4m3Pages, kI8Pages };
 
-// Two codes (bytes 0 and 1, or 2 and 3, of w) as numbers of type T, exactly.
-template <class T, int kHeld, bool kHigh>
-__device__ __forceinline__ uint32_t from_codes(uint32_t w) {
+// The four codes of w as numbers of type T, exactly.
+template <class T, int kHeld>
+__device__ __forceinline__ u32x2v from_codes(uint32_t w) {
     if constexpr (kHeld == kI8Pages)
-        return T::template from_i8<kHigh>(w);
+        return T::from_i8(w);
     else
-        return T::template from_e4m3<kHigh>(w);
+        return u32x2v{T::template from_e4m3<false>(w), T::template from_e4m3<true>(w)};
 }
 
 // The larger, and the sum, of a lane's value and that of the lane 16 (32) away.
@@ -218,6 +224,10 @@ struct AppendPagesArgs {
     float eps;
 };
 
+// Heads of one side that a workgroup of chunks takes.  The cosines of a page's tokens are made once for up to 16 heads; where
+// pages are few, for 4, on more workgroups (8 heads of 128: a prompt of 32,768 tokens on pages of 16 47.9 us with all heads
+// together and 55.5 with 4, of 64 56.0 and 60.5, of 128, 256 of them, 74.3 and 68.8; 64 runs of 6 tokens 5.9 and 5.3).
+inline uint32_t append_heads(uint64_t pages, uint32_t heads) { return pages * ((heads + 15u) / 16u) >= 512u ? 16u : 4u; }
 hipError_t launch_append_pages(const AppendPagesArgs& a, uint32_t dim, uint32_t type, bool int8, hipStream_t stream);
 hipError_t launch_norm_rope(const NormRopeArgs& a, uint32_t dim, uint32_t type, hipStream_t stream);
 hipError_t launch_append(const AppendArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);

@@ -195,7 +195,10 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         const int64_t blocks = (keys + kRowsBlock - 1) / kRowsBlock;
         const bool whole = blocks * d->cache->head_dim <= 512 || (groups >= 512 && blocks <= 8) || groups * blocks >> 31;
         const bool two = groups > 64 || (!good_type(d->cache->type) && d->cache->head_dim < 256);
-        f.n_work = whole ? 0u : static_cast<uint32_t>(std::min<uint64_t>(groups * blocks, two ? 512 : 256));
+        // Pages of codes with one scale, head_dim 64: there are registers for three workgroups on a CU (64 requests of up to
+        // 8,192 keys 77.7 us against 92.3; a third one does not help head_dim 128, 135 against 135, nor 256).
+        const bool three = two && of_pages(d->cache->type) && d->cache->head_dim == 64;
+        f.n_work = whole ? 0u : static_cast<uint32_t>(std::min<uint64_t>(groups * blocks, three ? 768 : two ? 512 : 256));
         if (f.n_work) {
             const size_t rows = size_t(f.n_work) * 2 * std::min(f.max_rows, kRowsTile);
             out->few_o = up256(rows * d->cache->head_dim * 4);
@@ -369,7 +372,9 @@ int engram_kv_append_pages(const engram_append_pages_desc* d, void* stream) {
     const bool each = per && (per * a.n_seq <= any || !d->cu_q);
     a.pages_per = each ? static_cast<uint32_t>(per) : 0u;
     // workgroups of 256 threads, and a grid has less than 2^32
-    if ((each ? per * a.n_seq : any) * ((2 * uint64_t(a.cache.n_kv_heads) + 15) / 16) >> 23) return ENGRAM_ERANGE;
+    const uint64_t pages = each ? per * a.n_seq : any;
+    const uint32_t heads = append_heads(pages, a.cache.n_kv_heads);
+    if (pages * (2 * ((uint64_t(a.cache.n_kv_heads) + heads - 1) / heads)) >> 23) return ENGRAM_ERANGE;
     if (bound == 1 && uint64_t(a.n_seq) * 2 * a.cache.n_kv_heads >> 24) return ENGRAM_ERANGE;
     a.rotary = d->rotary_dim;
     a.interleaved = d->interleaved;

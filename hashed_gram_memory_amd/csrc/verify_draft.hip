@@ -11,18 +11,22 @@
 // word may be 1e-6 and fp32 sums would now and then name its neighbour.
 //
 // The work is the reading of one row of p, and of q where a draft was refused:
-// HBM-bound for a batch, latency for one request.  (64 requests of 129,280
-// words in fp32: MEASURED)
+// HBM-bound for a batch, latency for one request.  64 requests of 5 drafts over
+// 129,280 words in fp32, 9 of 10 with a refused draft, take 19.2 us: 12 us of
+// sums (62 MB, 5.2 TB/s) and 7 to choose the word; one request takes 10.1 us,
+// over 4,096 words 6.4.
 //
 // Mapping: a row is taken in blocks of 4,096 words, 16 neighbours to each of
 // 256 threads.  One launch sums the blocks, a second finds the block in which
 // the sum passes v times the whole and reads that block again, thread sums
 // first and then the words of one thread.  Both launches sum in the same order,
-// so the block's end is the same number in both.  Rows of up to 32,768 words
-// take one launch, a workgroup of 1,024 threads to a row: reading the row by
-// itself takes a CU less time than the second launch does.
-// Which drafts are kept is a gather of K words and found anew by every
-// workgroup.
+// so the block's end is the same number in both.  Rows of up to 16,384 words
+// take one launch, a workgroup of 1,024 threads to a row (256 requests of 8,192
+// words 8.1 us against 12.9 in two launches, one of 4,096 6.4 against 9.9, 64 of
+// 16,384 9.7 against 10.7).  Eight words to a thread, or four waves on a SIMD
+// for five, take the same.
+// Which drafts are kept is a gather of K words, found anew by every workgroup
+// of the first launch.
 #include "drafts.h"
 #include "serving.h"
 
@@ -31,7 +35,7 @@ namespace {
 
 constexpr uint32_t kWords = 16;             // of a thread
 constexpr uint32_t kBlock = 256 * kWords;   // words of a block
-constexpr uint32_t kWhole = 1024 * 32;      // words of a row that one workgroup takes
+constexpr uint32_t kWhole = 1024 * kWords;  // words of a row that one workgroup takes
 
 struct F32 {
     static constexpr uint32_t kBytes = 4;
@@ -92,9 +96,8 @@ struct Verdict {
     uint32_t certain;        // the refused draft of a drafter that was certain, else none of the vocabulary
 };
 
-template <class E>
-__device__ __forceinline__ Verdict verdict_of(const VerifyArgs& A, uint32_t b) {
-    Verdict r;
+__device__ __forceinline__ Verdict drafts_of(const VerifyArgs& A, uint32_t b) {
+    Verdict r = {};
     if (A.cu_draft) {
         const int32_t n = static_cast<int32_t>(A.n_draft);
         const int32_t from = min(max(A.cu_draft[b], 0), n), to = min(max(A.cu_draft[b + 1], from), n);
@@ -104,8 +107,23 @@ __device__ __forceinline__ Verdict verdict_of(const VerifyArgs& A, uint32_t b) {
         r.first = b * A.uniform_drafts;
         r.count = A.uniform_drafts;
     }
+    return r;
+}
+
+// With `accepted` of them kept.
+__device__ __forceinline__ Verdict kept(const VerifyArgs& A, Verdict r, uint32_t b, uint32_t accepted) {
+    r.accepted = accepted;
+    r.refused = accepted < r.count;
+    r.row = r.first + accepted + b;
+    r.certain = r.refused && !A.drafter ? static_cast<uint32_t>(A.draft[r.first + accepted]) : UINT32_MAX;
+    return r;
+}
+
+template <class E>
+__device__ __forceinline__ Verdict verdict_of(const VerifyArgs& A, uint32_t b) {
+    const Verdict r = drafts_of(A, b);
     const uint32_t lane = threadIdx.x & 63u;
-    r.accepted = r.count;
+    uint32_t accepted = r.count;
     for (uint32_t i0 = 0; i0 < r.count; i0 += 64u) {
         const uint32_t i = i0 + lane;
         bool no = false;
@@ -120,14 +138,11 @@ __device__ __forceinline__ Verdict verdict_of(const VerifyArgs& A, uint32_t b) {
         }
         const uint64_t any = __ballot(no);
         if (any) {
-            r.accepted = i0 + static_cast<uint32_t>(__builtin_ctzll(any));
+            accepted = i0 + static_cast<uint32_t>(__builtin_ctzll(any));
             break;
         }
     }
-    r.refused = r.accepted < r.count;
-    r.row = r.first + r.accepted + b;
-    r.certain = r.refused && !A.drafter ? static_cast<uint32_t>(A.draft[r.first + r.accepted]) : UINT32_MAX;
-    return r;
+    return kept(A, r, b, accepted);
 }
 
 // The two kinds of weights of a word.
@@ -217,20 +232,47 @@ __device__ __forceinline__ void scan(Scan<kThreads>& sm, Weight mine, Weight& up
 
 __device__ __forceinline__ bool sound(double sum) { return sum > 0.0 && sum < __builtin_huge_val(); }
 
-// The first word of j0 .. j1 - 1 whose sum passes `goal`, else the last with a weight; `from`: the sum before j0.
+// The first of kWords words from j0 on, a lane's each, whose sum passes `goal`, else the last with a weight; `from`: the sum
+// before j0.
 template <class E>
-__device__ __forceinline__ uint32_t walk(const Rows& rows, uint32_t certain, bool of_w, uint32_t j0, uint32_t j1, double from,
-                                         double goal) {
-    uint32_t found = j0;
-    double sum = from;
-    for (uint32_t j = j0; j < j1; ++j) {
+__device__ __forceinline__ uint32_t word_of(const VerifyArgs& A, const Rows& rows, uint32_t certain, bool of_w, uint32_t j0,
+                                            double from, double goal) {
+    const uint32_t lane = threadIdx.x & 63u, j = j0 + lane;
+    double w = 0.0;
+    if (lane < kWords && j < A.vocab) {
         const Weight x = weight_of(E::at(rows.p, j), rows.q ? E::at(rows.q, j) : 0.0f, j == certain);
-        const double w = of_w ? x.w : x.p;
-        if (w > 0.0) found = j;
-        sum += w;
-        if (w > 0.0 && sum > goal) break;
+        w = of_w ? x.w : x.p;
     }
-    return found;
+    double upto = w;
+#pragma unroll
+    for (uint32_t k = 1; k < kWords; k <<= 1) {
+        const double y = __shfl_up(upto, k);
+        upto += lane >= k ? y : 0.0;
+    }
+    const uint64_t pass = __ballot(w > 0.0 && from + upto > goal), some = __ballot(w > 0.0);
+    return j0 + static_cast<uint32_t>(pass ? __builtin_ctzll(pass) : 63 - __builtin_clzll(some | 1u));
+}
+
+// The word at which a workgroup's sums pass the goal: the thread that holds it is found first (`w` its sum, `end` the sum to
+// its end), and its wave takes its words apart.
+template <class E>
+__device__ __forceinline__ uint32_t choose(const VerifyArgs& A, const Rows& rows, uint32_t certain, bool of_w, uint32_t first,
+                                           double w, double end, double goal, uint32_t* sm_found) {
+    // the first thread that passes; else the last that holds anything
+    const uint32_t rank = w > 0.0 ? (end > goal ? 4096u - threadIdx.x : 1u + threadIdx.x) : 0u;
+    if (rank) atomicMax(sm_found, rank);
+    __syncthreads();
+    const uint32_t best = *sm_found;
+    const uint64_t mine = __ballot(rank && rank == best);
+    __syncthreads();
+    if (mine) {
+        const int l = __builtin_ctzll(mine);
+        const uint32_t t = (threadIdx.x & ~63u) + static_cast<uint32_t>(l);
+        const uint32_t word = word_of<E>(A, rows, certain, of_w, first + t * kWords, __shfl(end - w, l), goal);
+        if ((threadIdx.x & 63u) == 0u) *sm_found = word;
+    }
+    __syncthreads();
+    return *sm_found;
 }
 
 __device__ __forceinline__ double goal_of(float v, double all) { return v > 0.0f ? static_cast<double>(v) * all : 0.0; }
@@ -243,7 +285,7 @@ __device__ __forceinline__ void put(const VerifyArgs& A, const Verdict& v, uint3
 }
 
 template <class E>
-__global__ __launch_bounds__(256) void sum_blocks_kernel(const VerifyArgs A) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(5))) void sum_blocks_kernel(const VerifyArgs A) {
     __shared__ Scan<256> sm;
     const uint32_t b = blockIdx.x / A.blocks, block = blockIdx.x - b * A.blocks;
     const Verdict v = verdict_of<E>(A, b);
@@ -253,6 +295,7 @@ __global__ __launch_bounds__(256) void sum_blocks_kernel(const VerifyArgs A) {
         double* const to = A.ws + 2 * static_cast<uint64_t>(blockIdx.x);
         to[0] = all.w;
         to[1] = all.p;
+        if (block == 0) A.accepted[b] = static_cast<int32_t>(v.accepted);
     }
 }
 
@@ -261,7 +304,7 @@ __global__ __launch_bounds__(256) void choose_kernel(const VerifyArgs A) {
     __shared__ Scan<256> sm;
     __shared__ uint32_t sm_found;
     const uint32_t b = blockIdx.x, lane = threadIdx.x & 63u;
-    const Verdict v = verdict_of<E>(A, b);
+    const Verdict v = kept(A, drafts_of(A, b), b, static_cast<uint32_t>(A.accepted[b]));
     const Rows rows = rows_of<E>(A, v);
     const double* const sums = A.ws + 2 * static_cast<uint64_t>(b) * A.blocks;
     // every wave for itself: the whole sum, in a fixed order, then the block in which it passes the goal
@@ -310,17 +353,9 @@ __global__ __launch_bounds__(256) void choose_kernel(const VerifyArgs A) {
     const Weight mine = sums_of<E>(A, rows, v.certain, j0);
     Weight upto, of_block;
     scan(sm, mine, upto, of_block);
-    // the first thread that passes; else the last that holds anything
     const double w = of_w ? mine.w : mine.p, end = before + (of_w ? upto.w : upto.p);
-    const uint32_t rank = w > 0.0 ? (end > goal ? 512u - threadIdx.x : 1u + threadIdx.x) : 0u;
-    if (rank) atomicMax(&sm_found, rank);
-    __syncthreads();
-    const uint32_t best = sm_found;
-    __syncthreads();
-    if (rank && rank == best)
-        sm_found = walk<E>(rows, v.certain, of_w, j0, min(j0 + kWords, A.vocab), end - w, goal);
-    __syncthreads();
-    put(A, v, b, static_cast<int32_t>(sm_found), 256);
+    const uint32_t word = choose<E>(A, rows, v.certain, of_w, block * kBlock, w, end, goal, &sm_found);
+    put(A, v, b, static_cast<int32_t>(word), 256);
 }
 
 template <class E>
@@ -330,14 +365,7 @@ __global__ __launch_bounds__(1024) void whole_kernel(const VerifyArgs A) {
     const uint32_t b = blockIdx.x;
     const Verdict v = verdict_of<E>(A, b);
     const Rows rows = rows_of<E>(A, v);
-    const uint32_t of_thread = A.vocab <= kWhole / 2 ? kWords : 2 * kWords, j0 = threadIdx.x * of_thread;
-    Weight mine = {0.0, 0.0};
-    if (j0 < A.vocab) mine = sums_of<E>(A, rows, v.certain, j0);
-    if (of_thread > kWords && j0 + kWords < A.vocab) {
-        const Weight more = sums_of<E>(A, rows, v.certain, j0 + kWords);
-        mine.w += more.w;
-        mine.p += more.p;
-    }
+    const Weight mine = sums_of<E>(A, rows, v.certain, threadIdx.x * kWords);
     if (threadIdx.x == 0) sm_found = 0;
     Weight upto, whole;
     scan(sm, mine, upto, whole);
@@ -349,14 +377,8 @@ __global__ __launch_bounds__(1024) void whole_kernel(const VerifyArgs A) {
     }
     const double goal = goal_of(A.last[b], all);
     const double w = of_w ? mine.w : mine.p, end = of_w ? upto.w : upto.p;
-    const uint32_t rank = w > 0.0 ? (end > goal ? 4096u - threadIdx.x : 1u + threadIdx.x) : 0u;
-    if (rank) atomicMax(&sm_found, rank);
-    __syncthreads();
-    const uint32_t best = sm_found;
-    __syncthreads();
-    if (rank && rank == best) sm_found = walk<E>(rows, v.certain, of_w, j0, min(j0 + of_thread, A.vocab), end - w, goal);
-    __syncthreads();
-    put(A, v, b, static_cast<int32_t>(sm_found), 1024);
+    const uint32_t word = choose<E>(A, rows, v.certain, of_w, 0, w, end, goal, &sm_found);
+    put(A, v, b, static_cast<int32_t>(word), 1024);
 }
 
 template <class E>

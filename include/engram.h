@@ -561,7 +561,8 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  * two requests of a call must not append to the same page.
  *
  * n_tok == 0 is a no-op.  Errors: EINVAL, ERANGE (n_tok / page_size + 2 n_seq
- * pages times n_kv_heads / 8 above 2^23: split the batch), EUNSUPPORTED (a type
+ * pages times n_kv_heads / 8, or n_seq * n_kv_heads of single tokens, above 2^23:
+ * split the batch), EUNSUPPORTED (a type
  * or geometry other than the above).
  */
 typedef struct engram_append_pages_desc {
