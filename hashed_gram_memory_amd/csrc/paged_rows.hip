@@ -44,7 +44,7 @@
 namespace engram {
 namespace {
 
-constexpr uint32_t kRows = kRowsTile;
+constexpr uint32_t kSet = kRowsTile;  // rows of one product: a tile has one set of them or two
 constexpr uint32_t kStep = 32;      // keys of a wave's step
 constexpr uint32_t kWaves = 4;
 
@@ -98,6 +98,7 @@ struct Load {
     uint32_t weight;   // of the request: 0 if it has no rows here
 };
 
+template <uint32_t kRows>
 __device__ __forceinline__ Load load_of(const AttentionArgs& A, uint32_t b) {
     Load l;
     l.req = request_of(A, b);
@@ -143,11 +144,12 @@ __device__ __forceinline__ void cut_share(Share& s, uint32_t all, uint32_t n_wor
 // This workgroup's share: a sum over the requests' loads, and the request in
 // which it begins.  Up to 64 requests each wave does it by itself, a request in
 // each lane, without LDS or a barrier.
+template <uint32_t kRows>
 __device__ __forceinline__ Share share_of(const AttentionArgs& A, ShareLds& sm) {
     Share s;
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     if (A.n_seq <= 64u) {
-        const uint32_t mine = lane < A.n_seq ? load_of(A, lane).weight : 0u;
+        const uint32_t mine = lane < A.n_seq ? load_of<kRows>(A, lane).weight : 0u;
         const uint32_t upto = sum_up_to(mine);
         cut_share(s, __builtin_amdgcn_readlane(upto, 63), A.n_work);
         s.b = static_cast<uint32_t>(__builtin_popcountll(__ballot(upto <= s.r0))) & 63u;
@@ -159,7 +161,7 @@ __device__ __forceinline__ Share share_of(const AttentionArgs& A, ShareLds& sm) 
     const uint32_t b0 = min(tid * per, A.n_seq), b1 = min(b0 + per, A.n_seq);
     uint32_t mine = 0;
 #pragma unroll 4
-    for (uint32_t b = b0; b < b1; ++b) mine += load_of(A, b).weight;
+    for (uint32_t b = b0; b < b1; ++b) mine += load_of<kRows>(A, b).weight;
     uint32_t upto = sum_up_to(mine);
     if (lane == 63u) sm.wave_sum[tid >> 6] = upto;
     __syncthreads();
@@ -175,7 +177,7 @@ __device__ __forceinline__ Share share_of(const AttentionArgs& A, ShareLds& sm) 
     if (s.r0 >= upto - mine && s.r0 < upto) {
         uint32_t at = upto - mine;
         for (uint32_t b = b0; b < b1; ++b) {
-            const uint32_t weight = load_of(A, b).weight;
+            const uint32_t weight = load_of<kRows>(A, b).weight;
             if (s.r0 < at + weight) {
                 sm.b = b;
                 sm.off = s.r0 - at;
@@ -190,9 +192,10 @@ __device__ __forceinline__ Share share_of(const AttentionArgs& A, ShareLds& sm) 
     return s;
 }
 
-template <class T, int D, int kHeld>
+template <class T, int D, int kHeld, int kSets>
 __global__ __launch_bounds__(kWaves * 64)
     __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : D == 64 ? 3 : 2))) void paged_rows_kernel(const AttentionArgs args) {
+    constexpr uint32_t kRows = kSets * kSet;
     constexpr bool kE4m3 = kHeld != kHalves;  // codes, of either kind
     constexpr bool kPages = kHeld == kE4m3Pages || kHeld == kI8Pages;  // one scale for a page and head
     constexpr int EPL = D / 16;              // channels of V in a lane
@@ -202,12 +205,12 @@ __global__ __launch_bounds__(kWaves * 64)
     // P and V's type.  A code is exact in bf16, whose range holds p * scale.
     using P = std::conditional_t<kE4m3, Bf16, T>;
     __shared__ ShareLds sm_share;
-    __shared__ float sm_o[kWaves * kRows * OP];
-    __shared__ float sm_m[kWaves][kRows], sm_l[kWaves][kRows];
+    __shared__ float sm_o[kWaves * kSet * OP];
+    __shared__ float sm_m[kWaves][kSet], sm_l[kWaves][kSet];
 
     Share share;
     if (args.n_work) {
-        share = share_of(args, sm_share);
+        share = share_of<kRows>(args, sm_share);
         if (threadIdx.x == 0) args.part_job[blockIdx.x] = int4{0, 0, 0, 0};
         if (share.r0 >= share.r1) return;
     } else {
@@ -228,7 +231,7 @@ __global__ __launch_bounds__(kWaves * 64)
         asm volatile("" : "+v"(tid));
         const uint32_t heads = A.cache.n_kv_heads;
         const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63u, n = lane & 15u, g = lane >> 4;
-        const Load load = load_of(A, share.b);
+        const Load load = load_of<kRows>(A, share.b);
         if (A.n_work && share.off >= load.weight) {  // the next request
             if (++share.b >= A.n_seq) return;
             share.off = 0;
@@ -257,11 +260,15 @@ __global__ __launch_bounds__(kWaves * 64)
         const int32_t c0 = load.lo + static_cast<int32_t>(block0) * kRowsBlock;
         const int32_t c1 = static_cast<int32_t>(min(static_cast<int64_t>(span.hi), c0 + static_cast<int64_t>(blocks) * kRowsBlock));
 
-        // this lane's row (column n of the products)
-        const uint32_t row = min(tile_row0 + n, rows - 1u);
-        const uint32_t tok = req.q0 + row / A.group, head = h * A.group + row % A.group;
-        const int32_t pos = req.kv_len - static_cast<int32_t>(req.q_len) + static_cast<int32_t>(row / A.group);
-        const int32_t see_lo = A.window && pos >= static_cast<int32_t>(A.window) ? pos - static_cast<int32_t>(A.window) + 1 : 0;
+        // this lane's row of each set (column n of the products)
+        const auto row_of = [&](int z) { return min(tile_row0 + kSet * z + n, rows - 1u); };
+        int32_t pos[kSets], see_lo[kSets];
+#pragma unroll
+        for (int z = 0; z < kSets; ++z) {
+            pos[z] = req.kv_len - static_cast<int32_t>(req.q_len) + static_cast<int32_t>(row_of(z) / A.group);
+            see_lo[z] = A.window && pos[z] >= static_cast<int32_t>(A.window) ? pos[z] - static_cast<int32_t>(A.window) + 1 : 0;
+        }
+        const auto there_is = [&](int z) { return z == 0 || n_rows > kSet; };  // rows of this set
         const uint32_t shift = A.cache.page_shift, in_page = (1u << shift) - 1u;
         const int32_t* __restrict__ table = A.table + (share.b) * A.table_stride;
         const int64_t of_head = static_cast<int64_t>(h) << shift;
@@ -322,23 +329,29 @@ __global__ __launch_bounds__(kWaves * 64)
             }
         };
 
-        u32x4v q[CH];
-        {
+        u32x4v q[kSets][CH];
+#pragma unroll
+        for (int z = 0; z < kSets; ++z) {
+            const uint32_t row = row_of(z), tok = req.q0 + row / A.group, head = h * A.group + row % A.group;
             const uint8_t* qp = A.q + (tok * A.q_tok + head * A.q_head) * 2;
 #pragma unroll
             for (uint32_t c = 0; c < CH; ++c) {
-                // e4m3 keys come 16 channels a load, which orders the channels of a pair of steps
+                // codes come 16 channels a load, which orders the channels of a pair of steps
                 const uint32_t d = kE4m3 ? 64 * (c / 2) + 16 * g + 8 * (c % 2) : 32 * c + 8 * g;
-                q[c] = *reinterpret_cast<const u32x4v*>(qp + d * 2);
+                q[z][c] = *reinterpret_cast<const u32x4v*>(qp + d * 2);
             }
         }
-        float m, nb, l;  // the reference (a score in units of log2), kShift - m once there is one, the sum
-        f32x4v o[EPL];
+        // the reference (a score in units of log2), kShift - m once there is one, the sum
+        float m[kSets], nb[kSets], l[kSets];
+        f32x4v o[kSets][EPL];
         for (bool careful = false;; careful = true) {
-            m = -INFINITY;
-            nb = l = 0.0f;
 #pragma unroll
-            for (int f = 0; f < EPL; ++f) o[f] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int z = 0; z < kSets; ++z) {
+                m[z] = -INFINITY;
+                nb[z] = l[z] = 0.0f;
+#pragma unroll
+                for (int f = 0; f < EPL; ++f) o[z][f] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+            }
             // The next step's keys are requested once this step's scores have used the registers, its values once the sums have.
             const int32_t first = c0 + static_cast<int32_t>(wave * kStep);
             Pages pages, ahead;
@@ -350,10 +363,11 @@ __global__ __launch_bounds__(kWaves * 64)
             }
             for (int32_t base = first; base < c1; base += kStep * kWaves) {
                 const int32_t next = base + static_cast<int32_t>(kStep * kWaves);
-                f32x4v s[2];
+                f32x4v s[kSets][2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    s[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int z = 0; z < kSets; ++z) s[z][t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (uint32_t c = 0; c < CH; ++c) {
                         u32x4v a;
@@ -364,18 +378,21 @@ __global__ __launch_bounds__(kWaves * 64)
                         } else {
                             a = u32x4v{kw[t][c].w[0], kw[t][c].w[1], kw[t][c].w[2], kw[t][c].w[3]};
                         }
-                        s[t] = T::mfma16(a, q[c], s[t]);
+#pragma unroll
+                        for (int z = 0; z < kSets; ++z) s[z][t] = T::mfma16(a, q[z][c], s[z][t]);
                     }
                 }
-                float x[2][4];
+                float x[kSets][2][4];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const float by = kPages ? A.scale_log2 * kp[t] : A.scale_log2;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[t][i] = s[t][i] * by;
-                        if constexpr (kE4m3 && !kPages) x[t][i] *= ks[t][i];
-                    }
+                    for (int z = 0; z < kSets; ++z)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[z][t][i] = s[z][t][i] * by;
+                            if constexpr (kE4m3 && !kPages) x[z][t][i] *= ks[t][i];
+                        }
                 }
                 if (next < c1) ask_k(next, ahead);
 
@@ -384,42 +401,46 @@ __global__ __launch_bounds__(kWaves * 64)
                                        ((g >> 1 ? pages.p[3] : pages.p[2]) >= 0 ? 0xFFFF0000u : 0u);
                 const bool whole = base >= last_row.lo && base + static_cast<int32_t>(kStep) <= min(first_row.hi, c1) &&
                                    (pages.p[0] | pages.p[1] | pages.p[2] | pages.p[3]) >= 0;
-                uint32_t seen = ~0u;  // keys base + 4g + bit that this lane's row sees (bits 0 to 3 and 16 to 19 are used)
-                if (!whole) {
-                    const int32_t from = base + static_cast<int32_t>(4u * g);
-                    seen = bits_of(see_lo - from, min(pos + 1, c1) - from) & there;
+                float p[kSets][2][4];
+                uint32_t seen[kSets];  // keys base + 4g + bit that this lane's row sees (bits 0 to 3 and 16 to 19 are used)
+#pragma unroll
+                for (int z = 0; z < kSets; ++z) {
+                    seen[z] = ~0u;
+                    if (!whole) {
+                        const int32_t from = base + static_cast<int32_t>(4u * g);
+                        seen[z] = bits_of(see_lo[z] - from, min(pos[z] + 1, c1) - from) & there;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[z][t][i] = (seen[z] >> (16 * t + i)) & 1u ? x[z][t][i] : -INFINITY;
+                    }
+                    float top = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[t][i] = (seen >> (16 * t + i)) & 1u ? x[t][i] : -INFINITY;
-                }
-                float top = -INFINITY;
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[z][t][i]);
+                    top = max32(max16(top));
+                    if (__any(top > m[z] + P::kSlack)) {
+                        const float m_new = fmaxf(m[z], top);
+                        const float nb_new = m_new == -INFINITY ? 0.0f : P::kShift - m_new;
+                        const float alpha = m[z] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(nb_new - nb[z]);
+                        l[z] *= alpha;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                        for (int f = 0; f < EPL; ++f)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[t][i]);
-                top = max32(max16(top));
-                if (__any(top > m + P::kSlack)) {
-                    const float m_new = fmaxf(m, top);
-                    const float nb_new = m_new == -INFINITY ? 0.0f : P::kShift - m_new;
-                    const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(nb_new - nb);
-                    l *= alpha;
+                            for (int i = 0; i < 4; ++i) o[z][f][i] *= alpha;
+                        m[z] = m_new;
+                        nb[z] = nb_new;
+                    }
 #pragma unroll
-                    for (int f = 0; f < EPL; ++f)
+                    for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[f][i] *= alpha;
-                    m = m_new;
-                    nb = nb_new;
-                }
-                float p[2][4];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[t][i] = __builtin_amdgcn_exp2f(x[t][i] + nb);
-                        l += p[t][i];
-                        if constexpr (kE4m3)
-                            p[t][i] = (seen >> (16 * t + i)) & 1u ? p[t][i] * (kPages ? vp[t] : vs[t][i]) : 0.0f;
+                        for (int i = 0; i < 4; ++i) {
+                            p[z][t][i] = __builtin_amdgcn_exp2f(x[z][t][i] + nb[z]);
+                            l[z] += p[z][t][i];
+                            if constexpr (kE4m3)
+                                p[z][t][i] = (seen[z] >> (16 * t + i)) & 1u ? p[z][t][i] * (kPages ? vp[t] : vs[t][i]) : 0.0f;
+                        }
                     }
                 }
 
@@ -458,7 +479,7 @@ __global__ __launch_bounds__(kWaves * 64)
                 if (__builtin_expect(careful && __any(bad != 0), 0)) {
                     // Key by key, V by way of LDS (the waves' sums use it only later): lane (n, g) adds p * V[its channels] for
                     // the keys that row n sees.  A loop of few registers, after which the products go on with zeros.
-                    uint32_t* const rows_v = reinterpret_cast<uint32_t*>(sm_o + wave * kRows * OP);
+                    uint32_t* const rows_v = reinterpret_cast<uint32_t*>(sm_o + wave * kSet * OP);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
 #pragma unroll
@@ -469,44 +490,51 @@ __global__ __launch_bounds__(kWaves * 64)
                     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                     __builtin_amdgcn_wave_barrier();
                     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+                    for (int z = 0; z < kSets; ++z)
 #pragma unroll 1
                     for (uint32_t k = 0; k < kStep; ++k) {
                         const int from = static_cast<int>(((k & 15u) >> 2) * 16u + n);
                         const uint32_t at = (k >> 4) * 4u + (k & 3u);
-                        float pk = p[0][0];
+                        float pk = p[z][0][0];
 #pragma unroll
-                        for (uint32_t z = 1; z < 8; ++z) pk = at == z ? p[z / 4][z % 4] : pk;
+                        for (uint32_t y = 1; y < 8; ++y) pk = at == y ? p[z][y / 4][y % 4] : pk;
                         pk = __shfl(pk, from);
-                        if ((static_cast<uint32_t>(__shfl(static_cast<int>(seen), from)) >> (16u * (k >> 4) + (k & 3u))) & 1u) {
+                        if ((static_cast<uint32_t>(__shfl(static_cast<int>(seen[z]), from)) >> (16u * (k >> 4) + (k & 3u))) & 1u) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
 #pragma unroll
                                 for (int e = 0; e < EPL / 2; ++e) {
                                     const uint32_t w = rows_v[k * (D / 2) + (4 * g + i) * (EPL / 2) + e];
-                                    o[2 * e][i] = __builtin_fmaf(pk, P::lo(w), o[2 * e][i]);
-                                    o[2 * e + 1][i] = __builtin_fmaf(pk, P::hi(w), o[2 * e + 1][i]);
+                                    o[z][2 * e][i] = __builtin_fmaf(pk, P::lo(w), o[z][2 * e][i]);
+                                    o[z][2 * e + 1][i] = __builtin_fmaf(pk, P::hi(w), o[z][2 * e + 1][i]);
                                 }
                         }
                     }
                 }
-                u32x4v ph, pl;
+                u32x4v ph[kSets], pl[kSets];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int z = 0; z < kSets; ++z)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float a = p[t][2 * i], b = p[t][2 * i + 1];
-                        const uint32_t w = P::pack(a, b);
-                        ph[2 * t + i] = w;
-                        pl[2 * t + i] = P::pack(a - P::lo(w), b - P::hi(w));
-                    }
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float a = p[z][t][2 * i], b = p[z][t][2 * i + 1];
+                            const uint32_t w = P::pack(a, b);
+                            ph[z][2 * t + i] = w;
+                            pl[z][2 * t + i] = P::pack(a - P::lo(w), b - P::hi(w));
+                        }
 #pragma unroll
                 for (int f = 0; f < EPL; ++f) {
                     u32x4v a;
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
                         a[w] = __builtin_amdgcn_perm(v[2 * w + 1].w[f / 2], v[2 * w].w[f / 2], (f & 1) ? 0x07060302u : 0x05040100u);
-                    o[f] = P::mfma16(a, ph, o[f]);
-                    o[f] = P::mfma16(a, pl, o[f]);
+#pragma unroll
+                    for (int z = 0; z < kSets; ++z) {
+                        o[z][f] = P::mfma16(a, ph[z], o[z][f]);
+                        o[z][f] = P::mfma16(a, pl[z], o[z][f]);
+                    }
                 }
                 if (next < c1) {
                     ask_v(next, ahead);
@@ -518,30 +546,39 @@ __global__ __launch_bounds__(kWaves * 64)
             // an infinity times a remainder of P.  The keys again, with their values looked at.
             bool nan = false;
 #pragma unroll
-            for (int f = 0; f < EPL; ++f)
+            for (int z = 0; z < kSets; ++z)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) nan |= o[f][i] != o[f][i];
+                for (int f = 0; f < EPL; ++f)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) nan |= o[z][f][i] != o[z][f][i];
             if (__builtin_expect(careful || !__any(nan), 1)) break;
         }
 
-        // join the waves
-        l = sum32(sum16(l));
-        if (g == 0) {
-            sm_m[wave][n] = m == -INFINITY ? m : -nb;
-            sm_l[wave][n] = l;
+        // join the waves, set by set
+#pragma unroll
+        for (int z = 0; z < kSets; ++z) {
+        if (z) {
+            if (!there_is(z)) break;
+            __syncthreads();  // LDS is read
         }
-        float* mine = sm_o + (wave * kRows + n) * OP + g * (D / 4);
-        if (n < n_rows) {
+        const uint32_t set_rows = min(kSet, n_rows - kSet * z);
+        l[z] = sum32(sum16(l[z]));
+        if (g == 0) {
+            sm_m[wave][n] = m[z] == -INFINITY ? m[z] : -nb[z];
+            sm_l[wave][n] = l[z];
+        }
+        float* mine = sm_o + (wave * kSet + n) * OP + g * (D / 4);
+        if (n < set_rows) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int f = 0; f < EPL; f += 4)
-                    *reinterpret_cast<f32x4v*>(mine + i * EPL + f) = f32x4v{o[f][i], o[f + 1][i], o[f + 2][i], o[f + 3][i]};
+                    *reinterpret_cast<f32x4v*>(mine + i * EPL + f) = f32x4v{o[z][f][i], o[z][f + 1][i], o[z][f + 2][i], o[z][f + 3][i]};
         }
         __syncthreads();
 
         const uint32_t at_row = tid >> 4, part = tid & 15u;  // row, EPL channels of it
-        if (at_row < n_rows) {
+        if (at_row < set_rows) {
             float top = -INFINITY;
 #pragma unroll
             for (uint32_t w = 0; w < kWaves; ++w) top = fmaxf(top, sm_m[w][at_row]);
@@ -553,20 +590,20 @@ __global__ __launch_bounds__(kWaves * 64)
             for (uint32_t w = 0; w < kWaves; ++w) {
                 const float f = __builtin_amdgcn_exp2f(sm_m[w][at_row] - ref);
                 sum += f * sm_l[w][at_row];
-                const float* src = sm_o + (w * kRows + at_row) * OP + part * EPL;
+                const float* src = sm_o + (w * kSet + at_row) * OP + part * EPL;
 #pragma unroll
                 for (int e = 0; e < EPL; ++e) acc[e] += f * src[e];
             }
             if (divided) {
                 const uint32_t place = 2u * blockIdx.x + (block0 == 0 ? 1u : 0u);
-                const uint64_t at = static_cast<uint64_t>(place) * min(A.max_rows, kRows) + at_row;
+                const uint64_t at = static_cast<uint64_t>(place) * min(A.max_rows, kRows) + kSet * z + at_row;
                 float* dst = A.part_o + at * D + part * EPL;
 #pragma unroll
                 for (int e = 0; e < EPL; e += 4)
                     *reinterpret_cast<f32x4v*>(dst + e) = f32x4v{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]};
                 if (part == 0) *reinterpret_cast<f32x2v*>(A.part_ml + at * 2) = f32x2v{top, sum};
             } else {
-                const uint32_t rr = tile_row0 + at_row;
+                const uint32_t rr = tile_row0 + kSet * z + at_row;
                 const uint32_t out_tok = req.q0 + rr / A.group, out_head = h * A.group + rr % A.group;
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 uint32_t w[EPL / 2];
@@ -579,6 +616,7 @@ __global__ __launch_bounds__(kWaves * 64)
                     A.lse[static_cast<uint64_t>(out_tok) * (heads * A.group) + out_head] =
                         sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
             }
+        }
         }
         if (r < share.r1) {
             __syncthreads();  // LDS is read
@@ -607,7 +645,7 @@ __global__ __launch_bounds__(256) void rows_join_kernel(const AttentionArgs A) {
     if (row >= rows) return;
     const uint32_t heads = A.cache.n_kv_heads;
     const uint32_t tok = req.q0 + row / A.group, head = h * A.group + row % A.group;
-    const uint32_t per = min(A.max_rows, kRows);
+    const uint32_t per = min(A.max_rows, A.of_tile);
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
     const auto place = [&](uint32_t s) {
         return static_cast<uint64_t>(2u * (blockIdx.x + s) + (s == 0 ? 1u : 0u)) * per + blockIdx.y;
@@ -652,14 +690,21 @@ __global__ __launch_bounds__(256) void rows_join_kernel(const AttentionArgs A) {
             sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
-template <class T, int D, int kHeld>
-hipError_t rows_one(const AttentionArgs& a, hipStream_t stream) {
-    const uint32_t groups = a.n_work ? a.n_work : tile_count<kRows>(a) * a.cache.n_kv_heads;
-    hipLaunchKernelGGL((paged_rows_kernel<T, D, kHeld>), dim3(groups), dim3(kWaves * 64), 0, stream, a);
+template <class T, int D, int kHeld, int kSets>
+hipError_t rows_sets(const AttentionArgs& a, hipStream_t stream) {
+    const uint32_t groups = a.n_work ? a.n_work : tile_count<kSets * kSet>(a) * a.cache.n_kv_heads;
+    hipLaunchKernelGGL((paged_rows_kernel<T, D, kHeld, kSets>), dim3(groups), dim3(kWaves * 64), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.n_work) return e;
-    hipLaunchKernelGGL((rows_join_kernel<T, D>), dim3(a.n_work, std::min(a.max_rows, kRows)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((rows_join_kernel<T, D>), dim3(a.n_work, std::min(a.max_rows, a.of_tile)), dim3(256), 0, stream, a);
     return hipGetLastError();
+}
+
+template <class T, int D, int kHeld>
+hipError_t rows_one(const AttentionArgs& a, hipStream_t stream) {
+    if constexpr (kHeld == kE4m3Pages || kHeld == kI8Pages)
+        if (a.of_tile == 2 * kSet) return rows_sets<T, D, kHeld, 2>(a, stream);
+    return rows_sets<T, D, kHeld, 1>(a, stream);
 }
 
 template <class T, int kHeld>

@@ -178,10 +178,12 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
     if (out->any_few) {
         AttentionArgs& f = out->few;
         f.max_rows = static_cast<uint32_t>(std::min<uint64_t>(most_rows, kFewRows));
-        f.tiles_per = (f.max_rows + kRowsTile - 1) / kRowsTile;
+        const bool sets = f.max_rows > kRowsTile && of_pages(d->cache->type);
+        f.of_tile = sets ? 2 * kRowsTile : kRowsTile;
+        f.tiles_per = (f.max_rows + f.of_tile - 1) / f.of_tile;
         // without a bound the tiles as the lengths need them may be fewer
-        if (!alike && uint64_t(f.n_tok) * group / kRowsTile + f.n_seq < uint64_t(f.tiles_per) * f.n_seq) f.tiles_per = 0;
-        const uint64_t groups = tile_count<kRowsTile>(f) * heads;
+        if (!alike && uint64_t(f.n_tok) * group / f.of_tile + f.n_seq < uint64_t(f.tiles_per) * f.n_seq) f.tiles_per = 0;
+        const uint64_t groups = (sets ? tile_count<2 * kRowsTile>(f) : tile_count<kRowsTile>(f)) * heads;
         if (groups > (uint64_t(1) << 23)) return ENGRAM_ERANGE;
         // Few keys: a workgroup takes a tile by itself, without the second launch that joins the parts (bf16, 8 KV heads,
         // head_dim 128: one request of 512 keys 8.2 us against 9.4 divided, of 1,024 12.5 against 9.5; where there are
@@ -200,7 +202,7 @@ int attention_args(const engram_attention_desc* d, Launches* out, size_t* ws_byt
         const bool three = two && of_pages(d->cache->type) && d->cache->head_dim == 64;
         f.n_work = whole ? 0u : static_cast<uint32_t>(std::min<uint64_t>(groups * blocks, three ? 768 : two ? 512 : 256));
         if (f.n_work) {
-            const size_t rows = size_t(f.n_work) * 2 * std::min(f.max_rows, kRowsTile);
+            const size_t rows = size_t(f.n_work) * 2 * std::min(f.max_rows, f.of_tile);
             out->few_o = up256(rows * d->cache->head_dim * 4);
             out->few_ml = up256(rows * 8);
             out->few_job = up256(f.n_work * sizeof(int4));

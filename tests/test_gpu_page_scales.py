@@ -162,3 +162,57 @@ def test_a_scale_of_nan_is_seen(new):
     out, lse = _attend(s, max_q_len=new)
     sees = torch.arange(64 - new, 64) >= 56
     assert torch.equal(out[:new].isnan().any(-1).any(-1).cpu(), sees) and out[new:].isfinite().all() and lse.isfinite().all()
+
+
+SETS = [
+    # kind, dtype, dim, kv heads, group, page, window, new tokens, kv lengths: 17 to 32 rows of a request, and fewer beside them
+    ("int8", BF16, 128, 8, 4, 16, 0, [6] * 3, [700, 6, 33]),
+    ("e4m3", BF16, 128, 2, 4, 32, 0, [6, 1, 0, 8, 4, 5], [3000, 40, 7, 8, 128, 4]),
+    ("int8", F16, 64, 2, 17, 8, 0, [1, 1], [999, 17]),
+    ("e4m3", F16, 64, 3, 5, 16, 40, [5, 6, 2], [300, 41, 39]),
+    ("int8", BF16, 256, 1, 8, 64, 0, [4, 3], [2500, 100]),
+    ("e4m3", F16, 256, 2, 3, 8, 100, [10, 7], [64, 1000]),
+    ("int8", BF16, 128, 1, 32, 16, 0, [1] * 5, [5000, 1, 0, 250, 129]),
+    ("int8", BF16, 64, 1, 1, 16, 0, [32, 17, 20], [9000, 17, 40]),
+]
+
+
+@pytest.mark.parametrize("case", SETS, ids=str)
+def test_two_sets_of_rows(case):
+    kind, dtype, D, H, G, page, window, new, lens = case
+    s = _coded(sum(new) + D + page, kind, dtype, D, H, G, page, new, lens, extra=1)
+    got = _attend(s, window, max_q_len=max(new))
+    _compare(s, got, window, 32)
+    again = _attend(s, window, max_q_len=max(new))
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    # one request by itself, whose rows the host knows
+    a, e = int(s["cu"][0]), int(s["cu"][1])
+    one = dict(s, q=s["q"][a:e], table=s["table"][:1], kv_len=s["kv_len"][:1], cu=s["cu"][:2], equal=True)
+    _compare(one, _attend(one, window), window, 32)
+
+
+@pytest.mark.parametrize("dim,group,new", [(128, 4, 6), (64, 2, 5), (256, 3, 9), (128, 4, 40)])
+def test_a_code_of_nan_is_seen(dim, group, new):
+    """By the tokens that see its key, in K and in V, in either set of rows; the others' results are what they would be."""
+    s = _coded(new + dim, "e4m3", BF16, dim, 2, group, 16, [new, 1], [150, 20])
+    for x in "kv":
+        bad = dict(s, **{x: s[x].clone()})
+        key = 150 - new + new // 2
+        bad[x][int(s["table"][0, key // 16]), 1, key % 16, 3] = 0x7F
+        out, lse = _attend(bad, max_q_len=new)
+        sees = torch.zeros(new + 1, 2 * group, dtype=torch.bool)
+        sees[new // 2:new, group:] = True
+        nan = sees[..., None].expand(out.shape).clone()
+        if x == "v":
+            nan[..., :3] = nan[..., 4:] = False
+            sees[:] = False
+        assert torch.equal(out.isnan().cpu(), nan) and torch.equal(lse.isnan().cpu(), sees)
+        # Against the form without the NaN where it does not reach.  (Not bit by bit against a call without it: V's products
+        # of a step that holds a NaN are added key by key, each within what _compare allows for P's two parts.)
+        k, v = (do.values(s[y], "e4m3") * s[y + "_scale"].double()[:, :, None, None] for y in "kv")
+        want, want_lse, _, _ = so.attention(s["q"], k, v, s["table"], s["kv_len"], s["cu"], dim ** -0.5, 0)
+        for b in range(2):
+            a, e = int(s["cu"][b]), int(s["cu"][b + 1])
+            one = dict(s, q=s["q"][a:e], table=s["table"][b:b + 1], kv_len=s["kv_len"][b:b + 1], cu=torch.tensor([0, e - a], dtype=torch.int32))
+            mended = torch.where(nan[a:e], want[a:e], out[a:e].double().cpu()), torch.where(sees[a:e], want_lse[a:e], lse[a:e].double().cpu())
+            _compare(one, mended, 0, (e - a) * group)
