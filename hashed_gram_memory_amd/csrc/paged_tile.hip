@@ -125,10 +125,11 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kMost) : "memory");
 }
 
-// eight codes as 16-bit numbers
-template <class T, int kHeld>
-__device__ __forceinline__ u32x4v widen(u32x2v w) {
-    const u32x2v a = from_codes<T, kHeld>(w[0]), b = from_codes<T, kHeld>(w[1]);
+// eight codes as 16-bit numbers, with their page's scale or without
+template <class T, int kHeld, bool kFold, bool kPlain>
+__device__ __forceinline__ u32x4v widen(u32x2v w, float scale) {
+    const u32x2v a = kFold ? scaled_codes<kHeld, kPlain>(w[0], scale) : from_codes<T, kHeld>(w[0]);
+    const u32x2v b = kFold ? scaled_codes<kHeld, kPlain>(w[1], scale) : from_codes<T, kHeld>(w[1]);
     return u32x4v{a[0], a[1], b[0], b[1]};
 }
 
@@ -137,6 +138,10 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     const AttentionArgs A) {
     constexpr bool kE4m3 = kHeld != kHalves;        // codes, of either kind
     constexpr bool kPages = kHeld == kE4m3Pages || kHeld == kI8Pages;  // one scale for a page and head
+    // A page's scale goes into its numbers as they are widened where bf16's range holds them: by way of the softmax, a chunk of
+    // 2,048 tokens over 32,768 keys took 1,375 us for 1,190 with e4m3 and 1,425 for 1,199 with int8.
+    constexpr bool kFold = kPages && std::is_same_v<T, Bf16>;
+    constexpr bool kScales = kE4m3 && !kFold;       // scales by way of LDS to the scores and weights
     constexpr uint32_t kRows = kWaves * 32u, kThreads = kWaves * 64u;
     constexpr bool kTurns = kWaves == 8;            // two waves of a workgroup on a SIMD
     constexpr int KT = kTurns || D == 64 ? 64 : 32; // keys of a tile
@@ -151,11 +156,11 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     constexpr float kSlack = P::kSlack, kShift = P::kShift;
     // With codes P is p_j times V's scale, which fp16's range does not hold under a reference of the scores alone: there the
     // reference is that of c s_j + log2(scale), with the logarithm bounded so that the sum of the p_j stays in fp32's range.
-    constexpr bool kScaled = kE4m3 && std::is_same_v<T, F16>;
+    constexpr bool kScaled = kScales && std::is_same_v<T, F16>;
 
     __shared__ __attribute__((aligned(1024))) uint16_t sm_k[4][KT * D];
     __shared__ __attribute__((aligned(1024))) uint16_t sm_v[5][KT * D];
-    __shared__ __attribute__((aligned(16))) float sm_scale[8][kScaled ? 3 : 2][kE4m3 ? KT : 4];
+    __shared__ __attribute__((aligned(16))) float sm_scale[kScales ? 8 : 1][kScaled ? 3 : 2][kScales ? KT : 4];
 
     const uint32_t heads = A.cache.n_kv_heads;
     const uint32_t tile_at = blockIdx.x / heads, h = blockIdx.x - tile_at * heads;
@@ -252,6 +257,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     struct Source {
         uint64_t k, v;
         uint32_t k_off, v_off;
+        int64_t scale_at;  // place of the page's scales (kFold)
     };
     struct Sources {
         Source of[NL];
@@ -267,6 +273,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
             const uint64_t none = reinterpret_cast<uint64_t>(g_zeros);
             r.of[i].k = ok ? reinterpret_cast<uint64_t>(kh + (p * A.cache.k_page_stride + in * D) * ES) : none;
             r.of[i].v = ok ? reinterpret_cast<uint64_t>(vh + (p * A.cache.v_page_stride + in * D) * ES) : none;
+            if constexpr (kFold) r.of[i].scale_at = (ok ? p : 0) * heads + h;  // (of zeros: any)
             const int32_t more = min(max(static_cast<int32_t>(lane / CB), span.lo - key), c1 - 1 - key);
             r.of[i].k_off = static_cast<uint32_t>(more) * (D * ES) + k_col;
             r.of[i].v_off = static_cast<uint32_t>(more) * (D * ES) + v_col;
@@ -285,23 +292,55 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     // e4m3: by way of registers, to be widened
     struct Blocks {
         u32x2v k[NL], v[NL];
+        float k_scale[NL], v_scale[NL];
     };
-    const auto ask = [&](const Sources& from) __attribute__((always_inline)) {
+    // Asked for where a turn reads nothing from LDS: while a scalar load is on its way, reads of LDS are waited for as one
+    // (1,224 us with the scales asked for among the products, 1,190 here, 1,280 by vector loads).
+    struct Scales {
+        float k[NL], v[NL];
+    };
+    const auto scales_of = [&](const Sources& from) __attribute__((always_inline)) {
+        Scales r;
+        if constexpr (kFold) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                r.k[i] = load_scalar(A.cache.k_scale + from.of[i].scale_at);
+                r.v[i] = load_scalar(A.cache.v_scale + from.of[i].scale_at);
+            }
+        }
+        return r;
+    };
+    const auto ask = [&](const Sources& from, const Scales& sc) __attribute__((always_inline)) {
         Blocks r;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             r.k[i] = *reinterpret_cast<const u32x2v*>(from.of[i].k + from.of[i].k_off);
             r.v[i] = *reinterpret_cast<const u32x2v*>(from.of[i].v + from.of[i].v_off);
+            if constexpr (kFold) {
+                r.k_scale[i] = sc.k[i];
+                r.v_scale[i] = sc.v[i];
+            }
         }
         return r;
     };
-    const auto put = [&](int32_t t, const Blocks& r) __attribute__((always_inline)) {
+    const auto put_as = [&](int32_t t, const Blocks& r, auto plain) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const uint32_t at = (i * kThreads + tid) * 8u;
-            *reinterpret_cast<u32x4v*>(&sm_k[t & 3][at]) = widen<T, kHeld>(r.k[i]);
-            *reinterpret_cast<u32x4v*>(&sm_v[static_cast<uint32_t>(t) % 5u][at]) = widen<P, kHeld>(r.v[i]);
+            *reinterpret_cast<u32x4v*>(&sm_k[t & 3][at]) = widen<T, kHeld, kFold, plain.value>(r.k[i], r.k_scale[i]);
+            *reinterpret_cast<u32x4v*>(&sm_v[static_cast<uint32_t>(t) % 5u][at]) = widen<P, kHeld, kFold, plain.value>(r.v[i], r.v_scale[i]);
         }
+    };
+    const auto put = [&](int32_t t, const Blocks& r) __attribute__((always_inline)) {
+        bool plain = true;
+        if constexpr (kFold && kHeld == kE4m3Pages) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) plain &= plain_scale(r.k_scale[i]) & plain_scale(r.v_scale[i]);
+        }
+        if (__builtin_expect(plain, 1))
+            put_as(t, r, std::true_type());
+        else
+            put_as(t, r, std::false_type());
     };
     // the scale of key tid % KT: of K (tid < KT), of V
     const auto ask_scale_page = [&](int32_t t) __attribute__((always_inline)) {
@@ -384,7 +423,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     };
     // scores to P; the sums follow the reference
     const auto softmax = [&](int32_t t) __attribute__((always_inline)) {
-        if constexpr (kE4m3) {
+        if constexpr (kScales) {
 #pragma unroll
             for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -446,7 +485,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
                 part[i & 1] += s[b][i];
             }
         l += part[0] + part[1];
-        if constexpr (kE4m3) {
+        if constexpr (kScales) {
 #pragma unroll
             for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -489,11 +528,14 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         int32_t scale_page = -1;
         const Sources f0 = sources_of(0, ask_pages(0)), f1 = sources_of(1, ask_pages(1)), f2 = sources_of(2, ask_pages(2));
         if constexpr (kE4m3) {
-            const Blocks b0 = ask(f0), b1 = ask(f1), b2 = ask(f2);
-            blocks = ask(sources_of(3, ask_pages(3)));
-            put_scale(0, ask_scale(0, ask_scale_page(0)));
-            scale = ask_scale(1, ask_scale_page(1));
-            scale_page = ask_scale_page(2);
+            const Blocks b0 = ask(f0, scales_of(f0)), b1 = ask(f1, scales_of(f1)), b2 = ask(f2, scales_of(f2));
+            const Sources f3 = sources_of(3, ask_pages(3));
+            blocks = ask(f3, scales_of(f3));
+            if constexpr (kScales) {
+                put_scale(0, ask_scale(0, ask_scale_page(0)));
+                scale = ask_scale(1, ask_scale_page(1));
+                scale_page = ask_scale_page(2);
+            }
             put(0, b0);
             put(1, b1);
             put(2, b2);
@@ -517,13 +559,16 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         // products, where a wave has instructions to spare.  Tiles past the last are brought too, and not read.
         const auto softmax_and_bring = [&](int32_t t, int32_t b, const Sources& from) __attribute__((always_inline)) {
             pages = ask_pages(b + 1 + kLead);
+            const Scales sc = scales_of(from);
             softmax(t);
             if constexpr (kE4m3) {
-                put_scale(b - 2, scale);
-                scale = ask_scale(b - 1, scale_page);
-                scale_page = ask_scale_page(b);
+                if constexpr (kScales) {
+                    put_scale(b - 2, scale);
+                    scale = ask_scale(b - 1, scale_page);
+                    scale_page = ask_scale_page(b);
+                }
                 put(b, blocks);
-                blocks = ask(from);
+                blocks = ask(from, sc);
             } else {
                 fetch(b, from);
             }
@@ -576,8 +621,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         for (int32_t t = 0; t < n_tiles; ++t) {
             const Sources from = sources_of(t, ask_pages(t));
             if constexpr (kE4m3) {
-                put(t, ask(from));
-                put_scale(t, ask_scale(t, ask_scale_page(t)));
+                put(t, ask(from, scales_of(from)));
+                if constexpr (kScales) put_scale(t, ask_scale(t, ask_scale_page(t)));
             } else {
                 fetch(t, from);
                 wait_loads<0>();

@@ -67,14 +67,20 @@ struct Bf16 : Halves<0x7F80u, 0x3F80u> {
     // four int8 codes likewise: their floats have no digits below this type's.  (The compiler takes a byte out of its word
     // first, and 3.25 instructions to a code where these are 1.5.)
     static __device__ __forceinline__ u32x2v from_i8(uint32_t w) {
-        uint32_t a, b, c, d;
+        float a, b, c, d;
+        bytes(w, a, b, c, d);
+        return u32x2v{halves(a, b), halves(c, d)};
+    }
+    static __device__ __forceinline__ void bytes(uint32_t w, float& a, float& b, float& c, float& d) {
         asm("v_cvt_f32_i32_sdwa %0, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0\n\t"
             "v_cvt_f32_i32_sdwa %1, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1\n\t"
             "v_cvt_f32_i32_sdwa %2, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2\n\t"
             "v_cvt_f32_i32_sdwa %3, sext(%4) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
             : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
             : "v"(w));
-        return u32x2v{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
+    }
+    static __device__ __forceinline__ uint32_t halves(float a, float b) {
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
     }
     // Softmax terms are held as 2^kShift at their row's reference, and may pass
     // it by 2^kSlack before the reference moves.
@@ -128,6 +134,29 @@ __device__ __forceinline__ u32x2v from_codes(uint32_t w) {
         return T::from_i8(w);
     else
         return u32x2v{T::template from_e4m3<false>(w), T::template from_e4m3<true>(w)};
+}
+
+// Whether a scale is a power of two that keeps bf16's numbers clear of the type's ends: no sign, no digits, 2^-101 to 2^100.
+__device__ __forceinline__ bool plain_scale(float scale) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, scale);
+    return (bits & 0x807FFFFFu) == 0u && bits - 0x0D000000u < 0x65000000u;
+}
+// The four codes of w times their page's scale as bf16: exact for a power of two, else rounded once.  kPlain: plain_scale
+// holds, and the conversion of e4m3 scales by itself.
+template <int kHeld, bool kPlain>
+__device__ __forceinline__ u32x2v scaled_codes(uint32_t w, float scale) {
+    if constexpr (kHeld == kI8Pages) {
+        float a, b, c, d;
+        Bf16::bytes(w, a, b, c, d);
+        return u32x2v{Bf16::pack(a * scale, b * scale), Bf16::pack(c * scale, d * scale)};
+    } else if constexpr (kPlain) {
+        return u32x2v{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true))};
+    } else {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+        return u32x2v{Bf16::pack(lo[0] * scale, lo[1] * scale), Bf16::pack(hi[0] * scale, hi[1] * scale)};
+    }
 }
 
 // The larger, and the sum, of a lane's value and that of the lane 16 (32) away.

@@ -606,7 +606,9 @@ int engram_kv_append_pages(const engram_append_pages_desc* desc, void* stream);
  * Products of 16-bit operands with fp32 sums; softmax in fp32.  For the second
  * product a_j is held in about 16 bits where a request has at most 32 rows (new
  * tokens * n_q_heads / n_kv_heads), and rounded once to `type` where it has
- * more.
+ * more.  There, with bf16 queries, codes times the scale of a page are held as
+ * bf16 too: exactly where the scale is a power of two, as the append writes them,
+ * else rounded once.
  *
  *   lse         device fp32 [n_tok][n_q_heads], or NULL.
  *   block_table device int32 [n_seq][table_width], rows table_stride apart.  A
