@@ -14,10 +14,10 @@
 //
 // Prompts: each row is read once and its codes are written once: HBM-bound.  A
 // prompt of 32,768 tokens (8 heads of 128, normed and turned, bf16) takes 48 us
-// on pages of 16, 4.2 TB/s, where a copy of 2 GiB reaches 4.8 to 4.9; 57 on
-// pages of 64, whose rows are read a second time, from L2, and turned a second
-// time.  Single tokens: launch-bound (64 of them 4.5 us, 4.2 of kernel), and
-// the page is touched only where its scale grows.
+// on pages of 16, 4.2 TB/s, where a copy of 2 GiB reaches 4.8 to 4.9, 50 on pages
+// of 64, and 75 on pages of 128, whose rows are read and turned twice; without
+// norm and rotation 45.  Single tokens: launch-bound (64 of them 4.0 to 4.6 us,
+// 4.2 of kernel), and the page is touched only where its scale grows.
 //
 // The norm's factor is the last product: it commutes with the rotation, x * w has
 // no rounding (two 16-bit numbers), and the page's factor is a power of two.  So
@@ -26,12 +26,14 @@
 //
 // Mapping: as in norm_rope.hip D/16 lanes hold a row of 16 elements each.
 //   * Chunks: a workgroup takes one page of one request and up to 16 heads of one
-//     side, a head to a wave in turn, so that the cosines of the page's tokens are
-//     made once for all its heads (by way of LDS).  Up to two steps of rows (16
-//     rows of head_dim 128) are held as they are turned, with the next head's on
-//     their way; of more rows the maximum is found first, and they are read and
-//     turned again (held in registers they took all of them: 114 us on pages of
-//     16, 86 on pages of 64).
+//     side, so that the cosines of the page's tokens are made once for all its
+//     heads (by way of LDS).  A wave holds two steps of rows (16 rows of head_dim
+//     128) as they are turned, with the next head's on their way; one, two or
+//     four waves share a head by the page's new rows, and their maxima go by way
+//     of LDS.  Of more rows than that (128, 64 and 32 of head_dim 64,
+//     128 and 256) the maximum is found first, and they are read and turned
+//     again.  (Pages of 64 read twice took 58 us; eight steps held by one wave as
+//     they were read took all registers, 86.)
 //   * Single tokens: a wave takes as many (head, side) pairs of a token as it
 //     holds rows.
 #include <algorithm>
@@ -205,7 +207,6 @@ struct Page {
     static constexpr uint32_t RPW = 64 / LPH, kHold = kSteps * RPW;  // rows of a step, rows whose cosines are held
     const AppendPagesArgs& A;
     f32x2v* cs;  // LDS: cosines and sines of kHold rows
-    float* fs;   // LDS: the norm's factors of kHold rows of each wave
     int64_t page;
     uint32_t row0, n_rows, tok0, head0, n_heads;
     uint32_t wave, lane, j, of_step, rb;
@@ -313,13 +314,15 @@ struct Page {
         }
     }
     // The page's scale, and the codes that it holds; the new rows' factor.
-    template <bool kKey>
+    // (kOf waves share the head.)
+    template <uint32_t kOf, bool kKey>
     __device__ __forceinline__ float settle(Pair<kKey> p, uint32_t most, float old) const {
         const Scale s = grown(scale_for<C>(most), old, row0 > 0u);
-        if (lane == 0) *scale_of(p) = s.now;
+        const uint32_t at = (wave & (kOf - 1u)) * 64u + lane;
+        if (at == 0) *scale_of(p) = s.now;
         if (s.ratio != 1.0f) {
             uint8_t* const codes = codes_of(p);
-            for (uint32_t i = lane * 16u; i < row0 * D; i += 1024u) {
+            for (uint32_t i = at * 16u; i < row0 * D; i += kOf * 1024u) {
                 u32x4v* const q = reinterpret_cast<u32x4v*>(codes + i);
                 *q = again<C>(*q, s.ratio);
             }
@@ -337,71 +340,73 @@ struct Page {
         if (r + of_step < n_rows) encode16<C>(codes_of(p) + static_cast<uint64_t>(row0 + r + of_step) * D, x, by, bl);
     }
 
-    // Up to two steps of rows: held as they are turned, the next head's on their way.
-    template <bool kKey>
-    __device__ __forceinline__ void few_rows() const {
+    // Up to two steps of rows to a wave: held as they are turned, the next head's on their way.  kOf waves share a head's rows,
+    // and the waves' maxima go by way of LDS (most: two sets of 4 words, used in turn, so that one barrier a head is enough).
+    template <uint32_t kOf, bool kKey>
+    __device__ __forceinline__ void held_rows(uint32_t* most) const {
+        constexpr uint32_t kAtOnce = 4u / kOf;
+        const uint32_t r = (wave & (kOf - 1u)) * 2u * RPW, first = wave / kOf;
         const auto ask = [&](uint32_t k, Raw* raw) {
             const Pair<kKey> p = {head0 + min(k, n_heads - 1u)};
-            raw[0] = load(p, 0);
-            raw[1] = load(p, RPW);
+            raw[0] = load(p, r);
+            raw[1] = load(p, r + RPW);
             return held_scale(p);
         };
         Raw next[2];
-        float next_old = ask(wave, next);
+        float next_old = ask(first, next);
         if (kKey) {
             make_turns(0);
             __syncthreads();
         }
-        for (uint32_t k = wave; k < n_heads; k += 4u) {
-            const Pair<kKey> p = {head0 + k};
+        const uint32_t rounds = (n_heads + kAtOnce - 1u) / kAtOnce;  // the same for all waves
+        for (uint32_t i = 0; i < (kOf == 1 ? (n_heads - min(first, n_heads) + 3u) / 4u : rounds); ++i) {
+            const uint32_t k = i * kAtOnce + first;
+            const bool live = kOf == 1 || k < n_heads;
+            const Pair<kKey> p = {head0 + min(k, n_heads - 1u)};
             float x[2][16], f[2];
             uint32_t m = 0;
 #pragma unroll
-            for (uint32_t i = 0; i < 2; ++i) {
-                f[i] = factor(next[i], p);
-                turned(next[i], p, i * RPW, 0, x[i]);
-                m = max(m, times(largest16(x[i]), f[i]));
+            for (uint32_t z = 0; z < 2; ++z) {
+                f[z] = factor(next[z], p);
+                turned(next[z], p, r + z * RPW, 0, x[z]);
+                m = max(m, times(largest16(x[z]), f[z]));
             }
             const float old = next_old;
-            if (k + 4u < n_heads) next_old = ask(k + 4u, next);
-            const float by = settle(p, wave_max(m), old);
-            put(x[0], p, 0, f[0] * by);
-            if (RPW < n_rows) put(x[1], p, RPW, f[1] * by);
+            if (k + kAtOnce < n_heads) next_old = ask(k + kAtOnce, next);
+            m = wave_max(m);
+            if constexpr (kOf > 1) {
+                uint32_t* const of_round = most + (i & 1u) * 4u;
+                if (lane == 0) of_round[wave] = m;
+                __syncthreads();
+#pragma unroll
+                for (uint32_t w = 0; w < kOf; ++w) m = max(m, of_round[(wave & ~(kOf - 1u)) + w]);
+            }
+            if (!live) continue;
+            const float by = settle<kOf>(p, m, old);
+            put(x[0], p, r, f[0] * by);
+            if (r + RPW < n_rows) put(x[1], p, r + RPW, f[1] * by);
         }
     }
 
-    // More: read twice, the second time from the caches.
+    // More, that are not turned: read twice, the second time from the caches.
     template <bool kKey>
     __device__ __forceinline__ void more_rows() const {
-        if (kKey) {
-            make_turns(0);
-            __syncthreads();
-        }
         for (uint32_t k = wave; k < n_heads; k += 4u) {
             const Pair<kKey> p = {head0 + k};
             const float old = held_scale(p);
-            const float by = settle(p, wave_max(largest_of(p, 0, n_rows)), old);
-            store_all(p, 0, n_rows, by, true);
+            const float by = settle<1>(p, wave_max(largest_of(p, 0, n_rows)), old);
+            store_all(p, 0, n_rows, by);
         }
     }
     template <bool kKey>
     __device__ __forceinline__ uint32_t largest_of(Pair<kKey> p, uint32_t r0, uint32_t r1) const {
         uint32_t m = 0;
-        float* const mine = fs + wave * kHold + of_step;  // a row's lanes all write its factor, and each reads its own word
-        each(p, r0, r1, [&](const Raw& raw, uint32_t r) {
-            const float f = factor(raw, p);
-            if (kKey && r - r0 < kHold) mine[r - r0] = f;
-            m = max(m, largest(raw, p, r, r0, f));
-        });
+        each(p, r0, r1, [&](const Raw& raw, uint32_t r) { m = max(m, largest(raw, p, r, r0, factor(raw, p))); });
         return m;
     }
     template <bool kKey>
-    __device__ __forceinline__ void store_all(Pair<kKey> p, uint32_t r0, uint32_t r1, float by, bool known) const {
-        const float* const mine = fs + wave * kHold + of_step;
-        each(p, r0, r1, [&](const Raw& raw, uint32_t r) {
-            const float f = !kKey ? 1.0f : known && r - r0 < kHold ? mine[r - r0] : factor(raw, p);
-            store(raw, p, r, r0, f * by);
-        });
+    __device__ __forceinline__ void store_all(Pair<kKey> p, uint32_t r0, uint32_t r1, float by) const {
+        each(p, r0, r1, [&](const Raw& raw, uint32_t r) { store(raw, p, r, r0, factor(raw, p) * by); });
     }
     // A head's rows step by step, kAhead steps on their way.
     template <bool kKey, class F>
@@ -436,7 +441,7 @@ struct Page {
                         const uint32_t m = wave_max(largest_of(p, r0, r1));
                         if (lane == 0) most[k] = max(most[k], m);  // the wave's own
                     } else {
-                        store_all(p, r0, r1, __builtin_bit_cast(float, most[k]), false);
+                        store_all(p, r0, r1, __builtin_bit_cast(float, most[k]));
                     }
                 }
             }
@@ -444,7 +449,7 @@ struct Page {
                 __syncthreads();
                 for (uint32_t k = wave; k < n_heads; k += 4u) {
                     const Pair<kKey> p = {head0 + k};
-                    const float by = settle(p, most[k], held_scale(p));
+                    const float by = settle<1>(p, most[k], held_scale(p));
                     if (lane == 0) most[k] = __builtin_bit_cast(uint32_t, by);
                 }
             }
@@ -454,8 +459,12 @@ struct Page {
     template <bool kKey>
     __device__ __forceinline__ void append(uint32_t* most) const {
         if (n_rows <= 2 * RPW)
-            few_rows<kKey>();
-        else if (n_rows <= kHold || !kKey || !rb)
+            held_rows<1, kKey>(most);
+        else if (n_rows <= 4 * RPW)
+            held_rows<2, kKey>(most);
+        else if (n_rows <= kHold)
+            held_rows<4, kKey>(most);
+        else if (!kKey || !rb)
             more_rows<kKey>();
         else
             in_parts<kKey>(most);
@@ -467,7 +476,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void a
                                                                                                            uint32_t heads_each) {
     using P = Page<T, D, C>;
     __shared__ __attribute__((aligned(16))) f32x2v sm_cs[P::kHold * (D / 2)];
-    __shared__ float sm_fs[4 * P::kHold];
     __shared__ uint32_t sm_most[kHeads];
     const uint32_t lane = threadIdx.x & 63u;
     uint32_t b, at;  // request, and which of its pages
@@ -496,7 +504,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void a
     const int64_t page = A.table[b * A.table_stride + in_table];
     if (page < 0 || page >= A.cache.n_pages) return;
     const uint32_t key0 = in_table << shift;
-    P p = {A, sm_cs, sm_fs};
+    P p = {A, sm_cs};
     p.page = page;
     p.row0 = max(static_cast<uint32_t>(lo), key0) - key0;
     p.n_rows = min(static_cast<uint32_t>(req.kv_len) - key0, 1u << shift) - p.row0;
@@ -609,7 +617,7 @@ hipError_t pages_one(const AppendPagesArgs& a, hipStream_t stream) {
     } else {
         const uint32_t pages = a.pages_per ? a.n_seq * a.pages_per : (a.n_tok >> a.cache.page_shift) + 2u * a.n_seq;
         const uint32_t heads = a.cache.n_kv_heads;
-        const uint32_t each = append_heads(pages, heads);
+        const uint32_t each = append_heads(pages, heads, a.rotary > 0);
         hipLaunchKernelGGL((append_pages_kernel<T, D, C>), dim3(pages, 2u * ((heads + each - 1u) / each)), dim3(256), 0, stream, a,
                            each);
     }

@@ -9,7 +9,12 @@
 // HBM-bound.  64 requests of up to 8,192 keys (8 KV heads, head_dim 128, bf16)
 // take 218 us, 5.6 TB/s, where a streaming read reaches 6.7 to 6.9, and over
 // e4m3 131 us, 4.8 TB/s; with all of them full 360 us, 6.0 TB/s, and 192 us,
-// 5.8 TB/s.
+// 5.8 TB/s.  Pages of codes with one scale take 128 us (e4m3) and 133 (int8,
+// 4.6 TB/s; full 192, 5.6): some 25 us of that are what any such call takes
+// beside its bytes (two launches, each share's first keys, two ends of tiles).
+// There 17 to 32 rows, as drafted tokens make them, are one tile of two sets:
+// each key is read and widened once for both (16 requests of 6 tokens, 4 heads to
+// a key, e4m3, 57 us against 67 in two tiles).
 //
 // Mapping (gfx950, wave64): a workgroup takes one tile of 16 rows of one KV
 // head and a run of its keys; its 4 waves take 32 keys each in turn, straight

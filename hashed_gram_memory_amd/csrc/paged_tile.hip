@@ -37,7 +37,9 @@
 //     against 1,109, for which the same chunk over 16 bits is 2% slower (678
 //     against 663).  A head_dim of 256 leaves registers for one wave on a SIMD:
 //     half tiles, one to a CU.  Over e4m3, whose tiles pass through registers,
-//     full tiles spill 6 registers and head_dim 256 some 65.
+//     full tiles spill 6 registers and head_dim 256 some 65.  Pages of codes with
+//     one scale have it in their numbers (bf16): there nothing but head_dim 256
+//     of e4m3 spills, some 32.
 //
 // What it measured, for 2,048 tokens at the end of 32,768 keys, 32 heads over 8
 // of head_dim 128, bf16: 1,314 us with two buffers, staged through registers,

@@ -254,9 +254,12 @@ struct AppendPagesArgs {
 };
 
 // Heads of one side that a workgroup of chunks takes.  The cosines of a page's tokens are made once for up to 16 heads; where
-// pages are few, for 4, on more workgroups (8 heads of 128: a prompt of 32,768 tokens on pages of 16 47.9 us with all heads
-// together and 55.5 with 4, of 64 56.0 and 60.5, of 128, 256 of them, 74.3 and 68.8; 64 runs of 6 tokens 5.9 and 5.3).
-inline uint32_t append_heads(uint64_t pages, uint32_t heads) { return pages * ((heads + 15u) / 16u) >= 512u ? 16u : 4u; }
+// pages are few or nothing is turned, for 4, on more workgroups (8 heads of 128: a prompt of 32,768 tokens on pages of 16 48.0
+// us with all heads together and 51.9 with 4, of 64 50.1 and 52.7, of 16 without rotation 47.1 and 44.8; 64 runs of 6 tokens
+// 5.9 and 4.6).
+inline uint32_t append_heads(uint64_t pages, uint32_t heads, bool turned) {
+    return turned && pages * ((heads + 15u) / 16u) >= 512u ? 16u : 4u;
+}
 hipError_t launch_append_pages(const AppendPagesArgs& a, uint32_t dim, uint32_t type, bool int8, hipStream_t stream);
 hipError_t launch_norm_rope(const NormRopeArgs& a, uint32_t dim, uint32_t type, hipStream_t stream);
 hipError_t launch_append(const AppendArgs& a, uint32_t dim, uint32_t type, bool e4m3, hipStream_t stream);

@@ -375,7 +375,7 @@ int engram_kv_append_pages(const engram_append_pages_desc* d, void* stream) {
     a.pages_per = each ? static_cast<uint32_t>(per) : 0u;
     // workgroups of 256 threads, and a grid has less than 2^32
     const uint64_t pages = each ? per * a.n_seq : any;
-    const uint32_t heads = append_heads(pages, a.cache.n_kv_heads);
+    const uint32_t heads = append_heads(pages, a.cache.n_kv_heads, d->rotary_dim > 0);
     if (pages * (2 * ((uint64_t(a.cache.n_kv_heads) + heads - 1) / heads)) >> 23) return ENGRAM_ERANGE;
     if (bound == 1 && uint64_t(a.n_seq) * 2 * a.cache.n_kv_heads >> 24) return ENGRAM_ERANGE;
     a.rotary = d->rotary_dim;

@@ -555,14 +555,14 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  * Rows of a page before a request's first new token count as held, those after
  * its last do not and are left as they are: a request whose tokens were
  * refused appends over them.  A token before the request's first key, and one
- * on a page number outside the pool, is left out, as are all past
- * max_q_len (0: not known) of a request.  kv_len is bounded by table_width *
+ * on a page number outside the pool, is left out; those past max_q_len (0: not
+ * known) of a request may be.  kv_len is bounded by table_width *
  * page_size, by 2^31 - 4096 and by 0.  A page is written for one request:
  * two requests of a call must not append to the same page.
  *
  * n_tok == 0 is a no-op.  Errors: EINVAL, ERANGE (n_tok / page_size + 2 n_seq
- * pages times n_kv_heads / 8, or n_seq * n_kv_heads of single tokens, above 2^23:
- * split the batch), EUNSUPPORTED (a type
+ * pages times n_kv_heads / 2, or n_seq * n_kv_heads of single tokens, may be
+ * refused above 2^23: split the batch), EUNSUPPORTED (a type
  * or geometry other than the above).
  */
 typedef struct engram_append_pages_desc {

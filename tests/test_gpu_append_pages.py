@@ -100,14 +100,21 @@ CASES = [
     ("e4m3", BF16, 256, 2, 128, 48, True, True, [150], [300]),
     ("int8", F16, 64, 3, 16, 16, False, True, [1, 1], [7, 500000]),
     ("e4m3", BF16, 128, 1, 256, 64, True, False, [700], [800]),
+    # two and four waves to a head, pages with rows before the first, more heads than a workgroup takes
+    ("e4m3", BF16, 128, 5, 64, 128, True, False, [100, 40, 20], [130, 45, 83]),
+    ("int8", F16, 64, 18, 128, 64, True, True, [200, 45], [290, 70]),
+    ("int8", BF16, 256, 3, 32, 64, True, False, [31, 12, 50], [40, 12, 60]),
+    ("e4m3", F16, 128, 6, 64, 0, False, False, [64, 33], [128, 40]),
+    ("int8", BF16, 128, 2, 16, 64, True, False, [9000], [9007]),  # pages enough for all heads together
+    ("e4m3", BF16, 64, 33, 32, 64, True, True, [9, 0, 12000], [20, 3, 12011]),
 ]
 
 
 @pytest.mark.parametrize("case", CASES, ids=str)
 def test_append(case):
     kind, dtype, D, H, page, R, norm, il, new, lens = case
-    s = _batch(sum(new) * 3 + D + page, kind, dtype, D, H, page, new, [min(n, 4000) for n in lens], R, norm, il)
-    s["positions"] += max(lens) - min(max(lens), 4000)
+    s = _batch(sum(new) * 3 + D + page, kind, dtype, D, H, page, new, [min(n, 13000) for n in lens], R, norm, il)
+    s["positions"] += max(lens) - min(max(lens), 13000)
     d = _device(s)
     _call(d)
     _compare(s, d, "by offsets")
