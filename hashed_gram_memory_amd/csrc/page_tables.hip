@@ -30,7 +30,7 @@ namespace engram {
 namespace {
 
 constexpr uint32_t kThreads = 1024, kWaves = kThreads / 64;
-constexpr uint32_t kCap = 1u << 30;  // sums end here: more tokens or pages than a call may have
+constexpr uint32_t kCap = INT32_MAX;  // sums end here: more tokens or pages than a call may have, and two do not wrap
 constexpr uint64_t kMostLength = INT32_MAX - 4095;  // keys of a request, as the attention takes them
 
 __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return min(a + b, kCap); }
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(const TablesArgs A) {
         taken[A.n_seq] = takes.all;
         back[A.n_seq] = backs.all;
     }
-    // the two counts as one sum: of pages below 2^30, of requests below 2^21
+    // the pages dealt and the requests that got none
     {
         const uint32_t lane = tid & 63u;
         uint32_t d = dealt, m = missed;

@@ -254,3 +254,21 @@ def test_slots_with_the_append_by_slots():
                                         torch.tensor([0, 1]), D ** -0.5, 0)
         bound, _ = so.attention_bounds(o, l, mass, move, BF16, P_SPLIT[BF16])
         _close(out[b:b + 1], o, bound, b)
+
+
+def test_a_stack_of_the_most_pages():
+    """2^30 free pages, and five requests that want 2^28 - 512 each: four get them, the fifth is not taken for served because
+    the sum of what they want is past what a call may have."""
+    hg = lib()
+    page, each = 8, (2 ** 31 - 4096) // 8
+    table = torch.full((5, each), -3, dtype=I32, device="cuda")
+    free = torch.arange(1 << 30, dtype=I32, device="cuda")
+    n_free = torch.tensor([1 << 30], dtype=I32, device="cuda")
+    lengths, held = torch.full((5,), each * page, dtype=I32, device="cuda"), _z(5)
+    out = hg.page_tables(lengths, _z(5), table, held, free, n_free, page, 1 << 21)
+    assert out[3].tolist() == [each * page] * 4 + [0] and out[4].tolist() == [1] and held.tolist() == [each] * 4 + [0]
+    assert n_free.tolist() == [(1 << 30) - 4 * each]
+    for b in range(4):  # from the top of the stack down
+        want = torch.arange((1 << 30) - 1 - b * each, (1 << 30) - 1 - (b + 1) * each, -1, dtype=I32, device="cuda")
+        assert torch.equal(table[b], want)
+    assert (table[4] == -3).all()
