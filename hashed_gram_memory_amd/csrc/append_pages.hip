@@ -14,15 +14,17 @@
 //
 // Prompts: each row is read once and its codes are written once: HBM-bound.  A
 // prompt of 32,768 tokens (8 heads of 128, normed and turned, bf16) takes 48 us
-// on pages of 16, 4.2 TB/s, where a copy of 2 GiB reaches 4.8 to 4.9, 50 on pages
-// of 64, and 75 on pages of 128, whose rows are read and turned twice; without
+// on pages of 16, 4.2 TB/s, where a copy of 2 GiB reaches 4.8 to 4.9, 51 on pages
+// of 64, and 76 on pages of 128, whose rows are read and turned twice; without
 // norm and rotation 45.  Single tokens: launch-bound (64 of them 4.0 to 4.6 us,
 // 4.2 of kernel), and the page is touched only where its scale grows.
 //
-// The norm's factor is the last product: it commutes with the rotation, x * w has
-// no rounding (two 16-bit numbers), and the page's factor is a power of two.  So
-// an element has the roundings of its rotation and one more, and the row's
-// largest element times the factor is the largest of the stored row.
+// Norm and rotation have the formula's roundings, x * r * w and two products and
+// a sum to each element, none of them fused: a key that a rounding has moved may
+// get the next code, and so keys get those of the same formula in other fp32 but
+// where the sum of squares differs (128 chunks of 512 tokens, 8 heads of 128, int8:
+// 0.24 of a million codes differ from PyTorch's, 0.82 with the rotation's products
+// fused and r as the last factor, which takes 1 us less on pages of 64).
 //
 // Mapping: as in norm_rope.hip D/16 lanes hold a row of 16 elements each.
 //   * Chunks: a workgroup takes one page of one request and up to 16 heads of one
@@ -167,6 +169,23 @@ __device__ __forceinline__ float inverse_root(float x) {
     return __builtin_amdgcn_rsqf(small ? x * 0x1p96f : x) * (small ? 0x1p48f : 1.0f);
 }
 
+// The rotation with each product and sum rounded by itself.
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+#pragma clang fp contract(off)
+    const float ac = a * c, bs = b * s, as = a * s, bc = b * c;
+    a = ac - bs;
+    b = as + bc;
+}
+__device__ __forceinline__ void turn_apart(float* x, const Turn& t, bool interleaved) {
+    if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn_pair(x[2 * e], x[2 * e + 1], t.c[e], t.s[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn_pair(x[e], x[8 + e], t.c[e], t.s[e]);
+    }
+}
+
 // A request's new tokens and the keys that they are.  Lengths are bounded by what exists.
 struct Fresh {
     uint32_t q0, q_len;
@@ -271,16 +290,15 @@ struct Page {
             cs[turn_at(row, q)] = cos_sin(static_cast<double>(A.positions[tok0 + r0 + row]) * A.inv_freq[q]);
         }
     }
-    // The row as it is to be stored but for the norm's factor, which commutes with the rotation and is left to the last
-    // product.  x * w has no rounding: 8 digits of each in bf16, 11 in fp16.
+    // The row as it is to be stored; f: its norm's factor.
     template <bool kKey>
-    __device__ __forceinline__ void turned(const Raw& h, Pair<kKey>, uint32_t r, uint32_t r0, float* x) const {
+    __device__ __forceinline__ void turned(const Raw& h, Pair<kKey>, uint32_t r, uint32_t r0, float f, float* x) const {
         unpack8<T>(h.w[0], x);
         unpack8<T>(h.w[1], x + 8);
         if constexpr (kKey) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] *= weight[e];
-            if (j < rb) turn_row(x, turn_for(min(r + of_step, n_rows - 1u) - r0), A.interleaved != 0);
+            for (int e = 0; e < 16; ++e) x[e] = x[e] * f * weight[e];
+            if (j < rb) turn_apart(x, turn_for(min(r + of_step, n_rows - 1u) - r0), A.interleaved != 0);
         }
     }
     template <bool kKey>
@@ -295,15 +313,12 @@ struct Page {
         return A.weight ? f : 1.0f;
     }
     // The largest magnitude of the row, by its bits.
-    static __device__ __forceinline__ uint32_t times(uint32_t magnitude, float f) {
-        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, magnitude) * f) & kMagnitude;
-    }
     template <bool kKey>
     __device__ __forceinline__ uint32_t largest(const Raw& h, Pair<kKey> p, uint32_t r, uint32_t r0, float f) const {
         if constexpr (kKey) {
             float x[16];
-            turned(h, p, r, r0, x);
-            return times(largest16(x), f);
+            turned(h, p, r, r0, f, x);
+            return largest16(x);
         } else {  // 16-bit magnitudes are in order as whole numbers
             u16x2v m = {0, 0};
 #pragma unroll
@@ -332,7 +347,7 @@ struct Page {
     template <bool kKey>
     __device__ __forceinline__ void store(const Raw& h, Pair<kKey> p, uint32_t r, uint32_t r0, float by) const {
         float x[16];
-        turned(h, p, r, r0, x);
+        turned(h, p, r, r0, factor(h, p), x);
         put(x, p, r, by);
     }
     template <bool kKey>
@@ -363,13 +378,12 @@ struct Page {
             const uint32_t k = i * kAtOnce + first;
             const bool live = kOf == 1 || k < n_heads;
             const Pair<kKey> p = {head0 + min(k, n_heads - 1u)};
-            float x[2][16], f[2];
+            float x[2][16];
             uint32_t m = 0;
 #pragma unroll
             for (uint32_t z = 0; z < 2; ++z) {
-                f[z] = factor(next[z], p);
-                turned(next[z], p, r + z * RPW, 0, x[z]);
-                m = max(m, times(largest16(x[z]), f[z]));
+                turned(next[z], p, r + z * RPW, 0, factor(next[z], p), x[z]);
+                m = max(m, largest16(x[z]));
             }
             const float old = next_old;
             if (k + kAtOnce < n_heads) next_old = ask(k + kAtOnce, next);
@@ -383,8 +397,8 @@ struct Page {
             }
             if (!live) continue;
             const float by = settle<kOf>(p, m, old);
-            put(x[0], p, r, f[0] * by);
-            if (r + RPW < n_rows) put(x[1], p, r + RPW, f[1] * by);
+            put(x[0], p, r, by);
+            if (r + RPW < n_rows) put(x[1], p, r + RPW, by);
         }
     }
 
@@ -406,7 +420,7 @@ struct Page {
     }
     template <bool kKey>
     __device__ __forceinline__ void store_all(Pair<kKey> p, uint32_t r0, uint32_t r1, float by) const {
-        each(p, r0, r1, [&](const Raw& raw, uint32_t r) { store(raw, p, r, r0, factor(raw, p) * by); });
+        each(p, r0, r1, [&](const Raw& raw, uint32_t r) { store(raw, p, r, r0, by); });
     }
     // A head's rows step by step, kAhead steps on their way.
     template <bool kKey, class F>
@@ -575,28 +589,27 @@ __global__ __launch_bounds__(256) void append_token_kernel(const AppendPagesArgs
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-    float x[16], f = 1.0f;
+    float x[16];
     unpack8<T>(raw[0], x);
     unpack8<T>(raw[1], x + 8);
-    if (side == 0) {  // the same for all lanes of a row; the norm's factor comes last, as above
+    if (side == 0) {  // the same for all lanes of a row
         if (A.weight) {
             float w[16], ss = 0.0f;
             const uint16_t* wp = reinterpret_cast<const uint16_t*>(A.weight);
             unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + bl.b0 * 8u), w);
             unpack8<T>(*reinterpret_cast<const u32x4v*>(wp + bl.b1 * 8u), w + 8);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                ss = __builtin_fmaf(x[e], x[e], ss);
-                x[e] *= w[e];
-            }
-            f = inverse_root(row_sum<LPH>(ss) * (1.0f / D) + A.eps);
+            for (int e = 0; e < 16; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
+            const float f = inverse_root(row_sum<LPH>(ss) * (1.0f / D) + A.eps);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = x[e] * f * w[e];
         }
-        if (j < rb) turn_row(x, turn_of(sm_cs[wave], j, rb, il), il);
+        if (j < rb) turn_apart(x, turn_of(sm_cs[wave], j, rb, il), il);
     }
-    const uint32_t m = row_max<LPH>(__builtin_bit_cast(uint32_t, __builtin_bit_cast(float, largest16(x)) * f) & kMagnitude);
+    const uint32_t m = row_max<LPH>(largest16(x));
     if (!live) return;
     const Scale s = grown(scale_for<C>(m), old, place > 0u);
-    encode16<C>(codes + static_cast<uint64_t>(place) * D, x, f * s.by, bl);
+    encode16<C>(codes + static_cast<uint64_t>(place) * D, x, s.by, bl);
     if (j == 0) *scale = s.now;
     if (s.ratio != 1.0f) {
 #pragma unroll 4
