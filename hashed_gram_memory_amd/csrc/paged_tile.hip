@@ -108,6 +108,7 @@ __device__ __forceinline__ void products_in_order() {
 
 // What the rows of pages that are none are read from.
 __device__ __attribute__((aligned(16))) const uint8_t g_zeros[4096] = {};
+__device__ const float g_one = 1.0f;  // and their scale
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return static_cast<uint32_t>(
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     struct Source {
         uint64_t k, v;
         uint32_t k_off, v_off;
-        int64_t scale_at;  // place of the page's scales (kFold)
+        int64_t scale_at;  // place of the page's scales, -1 where there is no page (kFold)
     };
     struct Sources {
         Source of[NL];
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
             const uint64_t none = reinterpret_cast<uint64_t>(g_zeros);
             r.of[i].k = ok ? reinterpret_cast<uint64_t>(kh + (p * A.cache.k_page_stride + in * D) * ES) : none;
             r.of[i].v = ok ? reinterpret_cast<uint64_t>(vh + (p * A.cache.v_page_stride + in * D) * ES) : none;
-            if constexpr (kFold) r.of[i].scale_at = (ok ? p : 0) * heads + h;  // (of zeros: any)
+            if constexpr (kFold) r.of[i].scale_at = ok ? p * heads + h : -1;
             const int32_t more = min(max(static_cast<int32_t>(lane / CB), span.lo - key), c1 - 1 - key);
             r.of[i].k_off = static_cast<uint32_t>(more) * (D * ES) + k_col;
             r.of[i].v_off = static_cast<uint32_t>(more) * (D * ES) + v_col;
@@ -305,9 +306,10 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         Scales r;
         if constexpr (kFold) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                r.k[i] = load_scalar(A.cache.k_scale + from.of[i].scale_at);
-                r.v[i] = load_scalar(A.cache.v_scale + from.of[i].scale_at);
+            for (int i = 0; i < NL; ++i) {  // of the zeros in the place of a page that is none: 1
+                const int64_t at = from.of[i].scale_at;
+                r.k[i] = load_scalar(at < 0 ? &g_one : A.cache.k_scale + at);
+                r.v[i] = load_scalar(at < 0 ? &g_one : A.cache.v_scale + at);
             }
         }
         return r;
