@@ -36,10 +36,11 @@
 //     66 us against 73 and a chunk of 2,048 over 32,768 keys of e4m3 1,001
 //     against 1,109, for which the same chunk over 16 bits is 2% slower (678
 //     against 663).  A head_dim of 256 leaves registers for one wave on a SIMD:
-//     half tiles, one to a CU.  Over e4m3, whose tiles pass through registers,
-//     full tiles spill 6 registers and head_dim 256 some 65.  Pages of codes with
-//     one scale have it in their numbers (bf16): there nothing but head_dim 256
-//     of e4m3 spills, some 32.
+//     half tiles, one to a CU.  Over codes, whose tiles pass through registers,
+//     full tiles spill 6 registers and head_dim 256 some 60; pages of codes with
+//     one scale, for bf16 queries, have it in their numbers, and there nothing
+//     but head_dim 256 of e4m3 spills, some 40 (and 2 of a full tile, outside of
+//     its loop).
 //
 // What it measured, for 2,048 tokens at the end of 32,768 keys, 32 heads over 8
 // of head_dim 128, bf16: 1,314 us with two buffers, staged through registers,
@@ -55,7 +56,12 @@
 // 2.1e-4 in fp16).  Twice the digits, as in paged_rows.hip, are half as many
 // products again, and here the products are what is waited for: with them the
 // chunk took 1,450 us for 1,097, the batch of 24 requests 72.0 for 62.7, the
-// chunk of head_dim 64 893 for 699.
+// chunk of head_dim 64 893 for 699.  Codes of bf16 queries do not need them: a
+// code is exact in fp16, and so P is, V's scales being powers of two near each
+// other (Near), an fp16 of 11 bits for bf16's 8; the output of the int8 chunk is
+// then off by what its own rounding does, 1.7e-3 of it for 2.2e-3.  The scales
+// are looked at before the first tile (1 to 2 us of a short call); the loop takes
+// the same instructions.
 //
 // What a row does not see: scores of hidden keys become -inf before the
 // maximum, and their p is 0.  A key that no row sees (past the end, before the
@@ -73,6 +79,7 @@ namespace engram {
 namespace {
 
 typedef short s16x4v __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4v lds_s16x4v;
 typedef __attribute__((address_space(3))) const u32x4v lds_u32x4v;
 
@@ -106,9 +113,8 @@ __device__ __forceinline__ void products_in_order() {
     __builtin_amdgcn_sched_group_barrier(kMfma, kAhead, 0);
 }
 
-// What the rows of pages that are none are read from.
+// What the rows of pages that are none, and their scales, are read from.
 __device__ __attribute__((aligned(16))) const uint8_t g_zeros[4096] = {};
-__device__ const float g_one = 1.0f;  // and their scale
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return static_cast<uint32_t>(
@@ -135,6 +141,36 @@ __device__ __forceinline__ u32x4v widen(u32x2v w, float scale) {
     const u32x2v b = kFold ? scaled_codes<kHeld, kPlain>(w[1], scale) : from_codes<T, kHeld>(w[1]);
     return u32x4v{a[0], a[1], b[0], b[1]};
 }
+template <int kHeld, bool kPlain>
+__device__ __forceinline__ u32x4v widen_near(u32x2v w, uint32_t by) {
+    const u32x2v a = shifted_codes<kHeld, kPlain>(w[0], by), b = shifted_codes<kHeld, kPlain>(w[1], by);
+    return u32x4v{a[0], a[1], b[0], b[1]};
+}
+
+// Of the scales of V's pages: whether fp16 numbers and weights hold all of them in one unit (near_scales).  The numbers take
+// 10 octaves with all of a code's digits.  A weight below 2^-14 is off by 2^-25, 2^-35 of its row's largest, which n keys of
+// 2^r times the scale of that one make n 2^(r - 35) of its value at the most: 2^-8, as bf16 weights would be off at the most,
+// for 10 octaves and 2^17 keys, and an octave less for each doubling from there.
+struct Near {
+    bool all;
+    int32_t top;  // exponent of the largest, 127 more
+};
+constexpr int32_t kNear = 10;  // octaves
+// A thread's part: the largest exponent, and 256 less the smallest, each 0 where there is none (a scale of 0 is near any);
+// what is no such scale has all bits.
+__device__ __forceinline__ uint32_t near_of(float scale) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, scale), e = bits >> 23;
+    const bool power = (bits & 0x807FFFFFu) == 0u && e - 27u <= 160u;  // 2^-100 to 2^60, and no digits
+    return power ? e | (256u - e) << 16 : bits ? ~0u : 0u;
+}
+__device__ __forceinline__ uint32_t near_both(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2t, a), __builtin_bit_cast(u16x2t, b)));
+}
+__device__ __forceinline__ Near near_scales(uint32_t x, uint32_t keys) {
+    const int32_t top = static_cast<int32_t>(x & 0xFFFFu), low = 256 - static_cast<int32_t>(x >> 16);
+    const int32_t most = min(kNear, kNear + 17 - (32 - __builtin_clz(max(keys, 2u) - 1u)));
+    return {x == 0u || (top < 256 && top - low <= most), x ? top : 127};
+}
 
 template <class T, int D, int kHeld, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2, D == 256 ? 1 : 2))) void paged_tile_kernel(
@@ -154,15 +190,17 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     constexpr int FB = D / 32;                      // blocks of 32 channels
     constexpr int NL = KT * CB / int(kThreads);     // blocks of K (and of V) that a thread brings
     static_assert(NL >= 1 && NL * int(kThreads) == KT * CB, "every thread brings the same");
-    using P = T;                                    // P and V's type; codes are exact in both types
     constexpr uint32_t ES = kE4m3 ? 1 : 2;
-    constexpr float kSlack = P::kSlack, kShift = P::kShift;
+    // P and V are of type T (codes are exact in both types), or with bf16 queries over pages whose scales are near each other
+    // of fp16 (Near), whose P has 2^10 to 2^15 at its row's largest: below 2^-14 it is off by 2^-35 of that at most.
+    constexpr float kSlack = kFold ? 5.0f : T::kSlack, kShift = kFold ? 10.0f : T::kShift;
     // With codes P is p_j times V's scale, which fp16's range does not hold under a reference of the scores alone: there the
     // reference is that of c s_j + log2(scale), with the logarithm bounded so that the sum of the p_j stays in fp32's range.
     constexpr bool kScaled = kScales && std::is_same_v<T, F16>;
 
     __shared__ __attribute__((aligned(1024))) uint16_t sm_k[4][KT * D];
     __shared__ __attribute__((aligned(1024))) uint16_t sm_v[5][KT * D];
+    __shared__ uint32_t sm_spread[kWaves];
     __shared__ __attribute__((aligned(16))) float sm_scale[kScales ? 8 : 1][kScaled ? 3 : 2][kScales ? KT : 4];
 
     const uint32_t heads = A.cache.n_kv_heads;
@@ -245,9 +283,9 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     };
     // The first key of the wave's rows i, or where all of them lie outside of [span.lo, c1), of rows in the run next to them.
     const auto key_of = [&](int32_t t, int i) __attribute__((always_inline)) {
-        const int64_t key = static_cast<int64_t>(base_of(t)) + wave_row + i * kStep;
+        const int32_t key = base_of(t) + static_cast<int32_t>(wave_row + i * kStep);  // (kMostKeys leaves room past the last)
         const int32_t low = (span.lo & ~7) + static_cast<int32_t>(wave_row & 7u);
-        return static_cast<int32_t>(min(max(key, static_cast<int64_t>(low)), static_cast<int64_t>(c1 - 1)));
+        return min(max(key, low), c1 - 1);
     };
     const auto ask_pages = [&](int32_t t) __attribute__((always_inline)) {
         Pages r;
@@ -260,7 +298,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     struct Source {
         uint64_t k, v;
         uint32_t k_off, v_off;
-        int64_t scale_at;  // place of the page's scales, -1 where there is no page (kFold)
+        const float *k_scale, *v_scale;  // of the page (kFold); of one that is none: 0
     };
     struct Sources {
         Source of[NL];
@@ -272,11 +310,15 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
             const int32_t key = key_of(t, i);
             const uint32_t in = static_cast<uint32_t>(key) & in_page;
             const int64_t p = pg.of[i];
-            const bool ok = p >= 0 && p < A.cache.n_pages;
+            const bool ok = static_cast<uint32_t>(pg.of[i]) < static_cast<uint32_t>(A.cache.n_pages);
             const uint64_t none = reinterpret_cast<uint64_t>(g_zeros);
             r.of[i].k = ok ? reinterpret_cast<uint64_t>(kh + (p * A.cache.k_page_stride + in * D) * ES) : none;
             r.of[i].v = ok ? reinterpret_cast<uint64_t>(vh + (p * A.cache.v_page_stride + in * D) * ES) : none;
-            if constexpr (kFold) r.of[i].scale_at = ok ? p * heads + h : -1;
+            if constexpr (kFold) {
+                const int64_t at = p * heads + h;
+                r.of[i].k_scale = ok ? A.cache.k_scale + at : reinterpret_cast<const float*>(g_zeros);
+                r.of[i].v_scale = ok ? A.cache.v_scale + at : reinterpret_cast<const float*>(g_zeros);
+            }
             const int32_t more = min(max(static_cast<int32_t>(lane / CB), span.lo - key), c1 - 1 - key);
             r.of[i].k_off = static_cast<uint32_t>(more) * (D * ES) + k_col;
             r.of[i].v_off = static_cast<uint32_t>(more) * (D * ES) + v_col;
@@ -306,10 +348,9 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         Scales r;
         if constexpr (kFold) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {  // of the zeros in the place of a page that is none: 1
-                const int64_t at = from.of[i].scale_at;
-                r.k[i] = load_scalar(at < 0 ? &g_one : A.cache.k_scale + at);
-                r.v[i] = load_scalar(at < 0 ? &g_one : A.cache.v_scale + at);
+            for (int i = 0; i < NL; ++i) {
+                r.k[i] = load_scalar(from.of[i].k_scale);
+                r.v[i] = load_scalar(from.of[i].v_scale);
             }
         }
         return r;
@@ -327,24 +368,41 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         }
         return r;
     };
-    const auto put_as = [&](int32_t t, const Blocks& r, auto plain) __attribute__((always_inline)) {
+    // V's scales in units of `unit`, 2^-5 of the largest (near): 2^-5 to 2^5, so that every code is a normal number of fp16.
+    uint32_t to_unit = 0;  // from a scale's exponent to that of its factor
+    const auto factor_of = [&](float scale, auto plain) __attribute__((always_inline)) {
+        const uint32_t bits = __builtin_bit_cast(uint32_t, scale);
+        if constexpr (kHeld == kI8Pages) {  // as fp16; from 0 far below 0, as the largest exponent is 27 at least
+            const uint32_t one = static_cast<uint32_t>(max(static_cast<int32_t>((bits >> 13) + to_unit), 0));
+            return one | one << 16;
+        } else {
+            return plain.value || bits ? bits + to_unit : 0u;
+        }
+    };
+    const auto put_as = [&](int32_t t, const Blocks& r, auto near, auto plain) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const uint32_t at = (i * kThreads + tid) * 8u;
             *reinterpret_cast<u32x4v*>(&sm_k[t & 3][at]) = widen<T, kHeld, kFold, plain.value>(r.k[i], r.k_scale[i]);
-            *reinterpret_cast<u32x4v*>(&sm_v[static_cast<uint32_t>(t) % 5u][at]) = widen<P, kHeld, kFold, plain.value>(r.v[i], r.v_scale[i]);
+            u32x4v* const v = reinterpret_cast<u32x4v*>(&sm_v[static_cast<uint32_t>(t) % 5u][at]);
+            if constexpr (near.value)
+                *v = widen_near<kHeld, plain.value>(r.v[i], factor_of(r.v_scale[i], plain));
+            else
+                *v = widen<T, kHeld, kFold, plain.value>(r.v[i], r.v_scale[i]);
         }
     };
-    const auto put = [&](int32_t t, const Blocks& r) __attribute__((always_inline)) {
+    const auto put = [&](int32_t t, const Blocks& r, auto near) __attribute__((always_inline)) {
         bool plain = true;
         if constexpr (kFold && kHeld == kE4m3Pages) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) plain &= plain_scale(r.k_scale[i]) & plain_scale(r.v_scale[i]);
+            for (int i = 0; i < NL; ++i)
+                plain &= plain_scale(r.k_scale[i]) & (near.value ? __builtin_bit_cast(uint32_t, r.v_scale[i]) != 0u
+                                                                 : plain_scale(r.v_scale[i]));
         }
         if (__builtin_expect(plain, 1))
-            put_as(t, r, std::true_type());
+            put_as(t, r, near, std::true_type());
         else
-            put_as(t, r, std::false_type());
+            put_as(t, r, near, std::false_type());
     };
     // the scale of key tid % KT: of K (tid < KT), of V
     const auto ask_scale_page = [&](int32_t t) __attribute__((always_inline)) {
@@ -364,6 +422,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
             if (tid >= KT && tid < 2u * KT) sm_scale[t & 7][2][tid % KT] = fminf(fmaxf(__log2f(fabsf(x)), -60.0f), 60.0f);
     };
 
+    float unit = 1.0f;      // of the sums
     bool all_there = true;  // all pages: else every tile is looked at as one that a mask cuts
     f32x16v s[TB];       // scores, then softmax terms
     u32x4v pw[KT / 16];  // P in 16 bits
@@ -400,7 +459,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         return u32x4v{w0[0], w0[1], w1[0], w1[1]};
     };
     // O^T += V^T P^T
-    const auto sums = [&](int32_t t) __attribute__((always_inline)) {
+    const auto sums = [&](int32_t t, auto near) __attribute__((always_inline)) {
+        using P = std::conditional_t<near.value, F16, T>;
         const uint32_t from = lds_address(&sm_v[static_cast<uint32_t>(t) % 5u][0]);
         uint32_t at[FB];
 #pragma unroll
@@ -426,7 +486,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         return seen;
     };
     // scores to P; the sums follow the reference
-    const auto softmax = [&](int32_t t) __attribute__((always_inline)) {
+    const auto softmax = [&](int32_t t, auto near) __attribute__((always_inline)) {
+        using P = std::conditional_t<near.value, F16, T>;
         if constexpr (kScales) {
 #pragma unroll
             for (int b = 0; b < TB; ++b)
@@ -530,81 +591,122 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         Blocks blocks;
         float scale = 0.0f;
         int32_t scale_page = -1;
-        const Sources f0 = sources_of(0, ask_pages(0)), f1 = sources_of(1, ask_pages(1)), f2 = sources_of(2, ask_pages(2));
-        if constexpr (kE4m3) {
-            const Blocks b0 = ask(f0, scales_of(f0)), b1 = ask(f1, scales_of(f1)), b2 = ask(f2, scales_of(f2));
-            const Sources f3 = sources_of(3, ask_pages(3));
-            blocks = ask(f3, scales_of(f3));
-            if constexpr (kScales) {
-                put_scale(0, ask_scale(0, ask_scale_page(0)));
-                scale = ask_scale(1, ask_scale_page(1));
-                scale_page = ask_scale_page(2);
+        Blocks b0, b1, b2;
+        const auto ask_first = [&]() __attribute__((always_inline)) {
+            const Sources f0 = sources_of(0, ask_pages(0)), f1 = sources_of(1, ask_pages(1)), f2 = sources_of(2, ask_pages(2));
+            if constexpr (kE4m3) {
+                b0 = ask(f0, scales_of(f0));
+                b1 = ask(f1, scales_of(f1));
+                b2 = ask(f2, scales_of(f2));
+                const Sources f3 = sources_of(3, ask_pages(3));
+                blocks = ask(f3, scales_of(f3));
+            } else {
+                fetch(0, f0);
+                fetch(1, f1);
+                fetch(2, f2);
             }
-            put(0, b0);
-            put(1, b1);
-            put(2, b2);
-        } else {
-            fetch(0, f0);
-            fetch(1, f1);
-            fetch(2, f2);
+        };
+        const auto put_first = [&](auto near) __attribute__((always_inline)) {
+            put(0, b0, near);
+            put(1, b1, near);
+            put(2, b2, near);
+        };
+        if constexpr (!kFold) ask_first();
+        if constexpr (kScales) {
+            put_scale(0, ask_scale(0, ask_scale_page(0)));
+            scale = ask_scale(1, ask_scale_page(1));
+            scale_page = ask_scale_page(2);
         }
+        if constexpr (kE4m3 && !kFold) put_first(std::false_type());
         // of the pages that some row sees: those behind a window may have been freed (2,048 tokens with a window of 1,001, 32
         // heads over 8 of 64, pages of 16: 32.1 us, and 42.1 where a page before the first seen key counted as missing)
         bool bad = false;
+        uint32_t spread = 0;  // of the pages that there are
+#pragma unroll 4
         for (uint32_t i = (static_cast<uint32_t>(max(c0, span.lo)) >> shift) + tid; i <= static_cast<uint32_t>(c1 - 1) >> shift; i += kThreads) {
             const int32_t p = table[i];
-            bad |= p < 0 || p >= A.cache.n_pages;
+            const bool none = p < 0 || p >= A.cache.n_pages;
+            bad |= none;
+            if constexpr (kFold)
+                if (!none) spread = near_both(spread, near_of(A.cache.v_scale[static_cast<int64_t>(p) * heads + h]));
+        }
+        if constexpr (kFold) {
+#pragma unroll
+            for (int k = 1; k < 64; k <<= 1) spread = near_both(spread, static_cast<uint32_t>(__shfl_xor(static_cast<int>(spread), k)));
+            if (lane == 0) sm_spread[wave] = spread;
         }
         all_there = !__syncthreads_or(bad);
-        if constexpr (!kE4m3) wait_loads<0>();
-        Pages pages = ask_pages(3 + kLead);
-        phase();
-        // softmax of tile t, and tile b brought; its pages were asked for a turn before, and its addresses made among the
-        // products, where a wave has instructions to spare.  Tiles past the last are brought too, and not read.
-        const auto softmax_and_bring = [&](int32_t t, int32_t b, const Sources& from) __attribute__((always_inline)) {
-            pages = ask_pages(b + 1 + kLead);
-            const Scales sc = scales_of(from);
-            softmax(t);
-            if constexpr (kE4m3) {
-                if constexpr (kScales) {
-                    put_scale(b - 2, scale);
-                    scale = ask_scale(b - 1, scale_page);
-                    scale_page = ask_scale_page(b);
-                }
-                put(b, blocks);
-                blocks = ask(from, sc);
-            } else {
-                fetch(b, from);
-            }
-        };
-        if (kTurns && wave >= kWaves / 2) phase();
-        Sources from = sources_of(3 + kLead, pages);
-        scores(0);
-        phase();
-        softmax_and_bring(0, 3, from);
-        phase();
-        // The loop's place in the 32 bytes that an instruction fetch takes: of the eight this is as good as any where an
-        // edit before it moves the loop by 4 bytes (0.3 to 2% between them; 2,048 tokens with a window of 4,090 145.4 us
-        // here and 148.3 two places on).
-        asm volatile(".p2align 5\n\t.rept 6\n\ts_nop 0\n\t.endr");
-        for (int32_t t = 0; t + 1 < n_tiles; ++t) {
-            __builtin_amdgcn_s_setprio(1);  // products first: they leave the other half enough of the issue slots
-            from = sources_of(t + 4 + kLead, pages);
-            scores(t + 1);
-            sums(t);
-            products_in_order<CH * TB, KT / 16 * FB>();
-            if constexpr (!kE4m3) {  // tile t + 2 is there when both halves are past this; of tile t + 3 nothing is needed yet
-                __builtin_amdgcn_sched_barrier(0);
-                wait_loads<2 * NL>();
-            }
-            __builtin_amdgcn_s_setprio(0);
-            phase();
-            softmax_and_bring(t + 1, t + 4, from);
-            phase();
+        if constexpr (kFold) {
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) spread = near_both(spread, sm_spread[w]);
         }
-        sums(n_tiles - 1);
+        const Near near_all = near_scales(__builtin_amdgcn_readfirstlane(spread), static_cast<uint32_t>(c1 - c0));
         if constexpr (!kE4m3) wait_loads<0>();
-        if (kTurns && wave < kWaves / 2) phase();
+        const auto keys = [&](auto near) __attribute__((always_inline)) {
+            if constexpr (kFold) {
+                ask_first();  // (before the look at V's scales they took registers that full tiles do not have, and no less time)
+                put_first(near);
+            }
+            Pages pages = ask_pages(3 + kLead);
+            phase();
+            // softmax of tile t, and tile b brought; its pages were asked for a turn before, and its addresses made among the
+            // products, where a wave has instructions to spare.  Tiles past the last are brought too, and not read.
+            const auto softmax_and_bring = [&](int32_t t, int32_t b, const Sources& from) __attribute__((always_inline)) {
+                pages = ask_pages(b + 1 + kLead);
+                const Scales sc = scales_of(from);
+                softmax(t, near);
+                if constexpr (kE4m3) {
+                    if constexpr (kScales) {
+                        put_scale(b - 2, scale);
+                        scale = ask_scale(b - 1, scale_page);
+                        scale_page = ask_scale_page(b);
+                    }
+                    put(b, blocks, near);
+                    blocks = ask(from, sc);
+                } else {
+                    fetch(b, from);
+                }
+            };
+            if (kTurns && wave >= kWaves / 2) phase();
+            Sources from = sources_of(3 + kLead, pages);
+            scores(0);
+            phase();
+            softmax_and_bring(0, 3, from);
+            phase();
+            // The loop's place in the 32 bytes that an instruction fetch takes: of the eight this is as good as any where an
+            // edit before it moves the loop by 4 bytes (0.3 to 2% between them; 2,048 tokens with a window of 4,090 145.4 us
+            // here and 148.3 two places on).
+            asm volatile(".p2align 5\n\t.rept 6\n\ts_nop 0\n\t.endr");
+            for (int32_t t = 0; t + 1 < n_tiles; ++t) {
+                __builtin_amdgcn_s_setprio(1);  // products first: they leave the other half enough of the issue slots
+                from = sources_of(t + 4 + kLead, pages);
+                scores(t + 1);
+                sums(t, near);
+                products_in_order<CH * TB, KT / 16 * FB>();
+                if constexpr (!kE4m3) {  // tile t + 2 is there when both halves are past this; of tile t + 3 nothing is needed yet
+                    __builtin_amdgcn_sched_barrier(0);
+                    wait_loads<2 * NL>();
+                }
+                __builtin_amdgcn_s_setprio(0);
+                phase();
+                softmax_and_bring(t + 1, t + 4, from);
+                phase();
+            }
+            sums(n_tiles - 1, near);
+            if constexpr (!kE4m3) wait_loads<0>();
+            if (kTurns && wave < kWaves / 2) phase();
+        };
+        if constexpr (kFold) {
+            if (__builtin_expect(near_all.all, 1)) {
+                to_unit = kHeld == kI8Pages ? static_cast<uint32_t>(20 - near_all.top) << 10 : static_cast<uint32_t>(132 - near_all.top) << 23;
+                unit = __builtin_bit_cast(float, static_cast<uint32_t>(near_all.top - 5) << 23);
+                keys(std::true_type());
+            } else {
+                keys(std::false_type());
+            }
+        } else {
+            keys(std::false_type());
+        }
     }
 
     // A NaN in the sums may be there by right, or come from 0 * infinity or 0 * NaN of a value that its row's mask hides:
@@ -615,8 +717,10 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
 #pragma unroll
         for (int i = 0; i < 16; ++i) nan |= o[f][i] != o[f][i];
     if (__builtin_expect(__syncthreads_or(nan), 0)) {
+        using P = T;
         m = -INFINITY;
         nb = l = 0.0f;
+        unit = 1.0f;
 #pragma unroll
         for (int f = 0; f < FB; ++f)
 #pragma unroll
@@ -625,7 +729,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
         for (int32_t t = 0; t < n_tiles; ++t) {
             const Sources from = sources_of(t, ask_pages(t));
             if constexpr (kE4m3) {
-                put(t, ask(from, scales_of(from)));
+                put(t, ask(from, scales_of(from)), std::false_type());
                 if constexpr (kScales) put_scale(t, ask_scale(t, ask_scale_page(t)));
             } else {
                 fetch(t, from);
@@ -634,7 +738,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
             phase();
             {
                 scores(t);
-                softmax(t);
+                softmax(t, std::false_type());
                 const uint64_t seen = seen_of(t);
                 const uint32_t at_v = lds_address(&sm_v[static_cast<uint32_t>(t) % 5u][0]);
 #pragma unroll
@@ -674,6 +778,12 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
 
     l = sum32(l);
     if (!alive || wrow0 + n >= rows) return;
+    if constexpr (kFold) {
+#pragma unroll
+        for (int f = 0; f < FB; ++f)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[f][i] *= unit;
+    }
     const uint32_t q_heads = heads * A.group;
     const uint64_t flat = static_cast<uint64_t>(tok) * q_heads + head;
     if (divided) {

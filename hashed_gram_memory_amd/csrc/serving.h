@@ -159,6 +159,29 @@ __device__ __forceinline__ u32x2v scaled_codes(uint32_t w, float scale) {
     }
 }
 
+// The four codes of w times a power of two of 2^-5 to 2^5 as fp16, exactly, or times 0 (kPlain: it is not).  int8: the factor
+// comes as a pair of fp16, e4m3: as fp32.
+template <int kHeld, bool kPlain>
+__device__ __forceinline__ u32x2v shifted_codes(uint32_t w, uint32_t by) {
+    if constexpr (kHeld == kI8Pages) {
+        // 1,024 + 128 + the code by its bits, times the factor, less 1,152 of it: each exact
+        const _Float16 off = static_cast<_Float16>(-1152.0f);
+        const f16x2v f = __builtin_bit_cast(f16x2v, by), less = f * f16x2v{off, off};
+        const uint32_t u = w ^ 0x80808080u;
+        const f16x2v a = __builtin_bit_cast(f16x2v, __builtin_amdgcn_perm(u, 0x64646464u, 0x00050004u));
+        const f16x2v b = __builtin_bit_cast(f16x2v, __builtin_amdgcn_perm(u, 0x64646464u, 0x00070006u));
+        return u32x2v{__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(a, f, less)),
+                      __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(b, f, less))};
+    }
+    const float x = __builtin_bit_cast(float, by);
+    if constexpr (kPlain)
+        return u32x2v{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, x, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, x, true))};
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+    return u32x2v{F16::pack(lo[0] * x, lo[1] * x), F16::pack(hi[0] * x, hi[1] * x)};
+}
+
 // The larger, and the sum, of a lane's value and that of the lane 16 (32) away.
 __device__ __forceinline__ f32x2v swap16(float x) {
     const uint32_t w = __builtin_bit_cast(uint32_t, x);

@@ -606,9 +606,13 @@ int engram_kv_append_pages(const engram_append_pages_desc* desc, void* stream);
  * Products of 16-bit operands with fp32 sums; softmax in fp32.  For the second
  * product a_j is held in about 16 bits where a request has at most 32 rows (new
  * tokens * n_q_heads / n_kv_heads), and rounded once to `type` where it has
- * more.  There, with bf16 queries, codes times the scale of a page are held as
- * bf16 too: exactly where the scale is a power of two, as the append writes them,
- * else rounded once.
+ * more.  There, with bf16 queries over pages of codes with one scale, K's codes
+ * times their page's scale are held as bf16: exactly where the scale is a power of
+ * two, as the append writes them, else rounded once.  V's codes are exact, and a_j
+ * is rounded to fp16's 11 bits, where the scales of V's pages that some hundred
+ * rows see are 0 or powers of two from 2^-100 to 2^60, the largest 2^10 times the
+ * smallest at most (2^27 / n where they see n > 2^17 keys).  Else V is held as K
+ * is, and a_j rounded to bf16.
  *
  *   lse         device fp32 [n_tok][n_q_heads], or NULL.
  *   block_table device int32 [n_seq][table_width], rows table_stride apart.  A
