@@ -87,6 +87,9 @@ __device__ __forceinline__ Words16<Half<T>> load16(const uint8_t* row, uint32_t 
     return r;
 }
 
+// What a probability weighs: nothing if it is negative or NaN.
+__device__ __forceinline__ float weighs(float x) { return fmaxf(x, 0.0f); }
+
 // The drafts of a request, and what became of them.
 struct Verdict {
     uint32_t first, count;   // drafts first .. first + count - 1
@@ -131,8 +134,8 @@ __device__ __forceinline__ Verdict verdict_of(const VerifyArgs& A, uint32_t b) {
             const uint32_t t = r.first + i, d = static_cast<uint32_t>(A.draft[t]);
             float p = 0.0f, q = 1.0f;
             if (d < A.vocab) {
-                p = E::at(A.target + static_cast<uint64_t>(t + b) * A.target_stride * E::kBytes, d);
-                if (A.drafter) q = E::at(A.drafter + static_cast<uint64_t>(t) * A.drafter_stride * E::kBytes, d);
+                p = weighs(E::at(A.target + static_cast<uint64_t>(t + b) * A.target_stride * E::kBytes, d));
+                if (A.drafter) q = weighs(E::at(A.drafter + static_cast<uint64_t>(t) * A.drafter_stride * E::kBytes, d));
             }
             no = !(static_cast<double>(A.uniform[t]) * static_cast<double>(q) < static_cast<double>(p));
         }
@@ -150,8 +153,9 @@ struct Weight {
     double w, p;
 };
 __device__ __forceinline__ Weight weight_of(float p, float q, bool certain) {
-    const double x = p > 0.0f ? static_cast<double>(p) : 0.0;
-    return {certain ? 0.0 : p > q ? static_cast<double>(p) - static_cast<double>(q) : 0.0, x};
+    p = weighs(p);
+    q = weighs(q);
+    return {certain ? 0.0 : p > q ? static_cast<double>(p) - static_cast<double>(q) : 0.0, static_cast<double>(p)};
 }
 
 struct Rows {

@@ -749,8 +749,9 @@ int engram_page_tables(const engram_page_tables_desc* desc, void* ws, size_t ws_
  * draft_probs NULL: the drafts were certain (q_i is 1 at d_i, 0 elsewhere).
  * Products, differences and sums are fp64.  Rows need not be normalised.  A
  * draft that is no word (negative, or vocab and above) is refused; a negative
- * or NaN probability weighs nothing; next is -1 where the row's sum is not
- * positive and finite, and always a word with a weight where it is.
+ * or NaN probability counts as 0, the target's and the drafter's; next is -1
+ * where the row's sum is not positive and finite, and always a word with a weight
+ * where it is.
  *
  *   target      device [n_draft + n_seq][vocab] of `type` (ENGRAM_F32, BF16 or
  *               F16), rows target_stride elements apart, aligned as its elements.
