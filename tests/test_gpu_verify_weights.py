@@ -1,5 +1,6 @@
 """What probabilities weigh in the verification of drafts, those that are none among them, from the declaration alone: a
-negative or NaN probability weighs nothing, in the target as in the drafter."""
+negative or NaN probability weighs nothing, in the target as in the drafter; and what a call writes, byte by byte."""
+import ctypes
 import math
 
 import pytest
@@ -99,3 +100,37 @@ def test_a_drafter_that_gave_a_draft_nothing(vocab):
     for b, q in enumerate((math.nan, -1.0, 0.0)):
         s["q"][b, int(s["draft"][b])] = q
     assert _run(s) == _declared(s) and _run(s)[1] == [1, 1, 1]
+
+
+@pytest.mark.parametrize("vocab", [500, 20001])
+@pytest.mark.parametrize("certain", [False, True])
+def test_what_is_written(vocab, certain):
+    """Whatever the offsets say, the outputs' own places and the workspace's, and nothing beside them."""
+    from hashed_gram_memory_amd import serving as sv
+    s = _batch([2, 3, 1], vocab, F32, 4, certain=certain)
+    d = {k: None if v is None else v.cuda() for k, v in s.items()}
+    n_seq, n_draft, mark = 3, 6, 64
+    tokens = torch.full((mark + n_draft + n_seq + mark,), 0x5A5A5A5A, dtype=torch.int32, device="cuda")
+    accepted = torch.full((mark + n_seq + mark,), 0x5A5A5A5A, dtype=torch.int32, device="cuda")
+    for cu in ([0, 2, 5, 6], [-5, 2, 100, 3], [0, 7, 2, 6], [6, 6, 6, 6], [2 ** 31 - 1, -2 ** 31, 0, 2 ** 31 - 1], [3, 3, 6, 6]):
+        tokens.fill_(0x5A5A5A5A)
+        accepted.fill_(0x5A5A5A5A)
+        offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        desc = sv.VerifyDraftDesc(target=d["target"].data_ptr(), draft_probs=0 if certain else d["q"].data_ptr(),
+                                  draft=d["draft"].data_ptr(), uniform=d["uniform"].data_ptr(), last_uniform=d["last"].data_ptr(),
+                                  cu_draft=offsets.data_ptr(), tokens=tokens[mark:].data_ptr(),
+                                  n_accepted=accepted[mark:].data_ptr(), n_seq=n_seq, n_draft=n_draft, vocab=vocab,
+                                  target_stride=vocab, draft_stride=0 if certain else vocab, type=sv.F32)
+        need = ctypes.c_size_t()
+        assert sv._lib.engram_verify_draft_workspace(ctypes.byref(desc), ctypes.byref(need)) == 0
+        ws = torch.full((need.value + 1024,), 0x5A, dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.current_stream().cuda_stream
+        assert sv._lib.engram_verify_draft(ctypes.byref(desc), ws.data_ptr(), need.value, stream) == 0
+        torch.cuda.synchronize()
+        for x, n in ((tokens, n_draft + n_seq), (accepted, n_seq)):
+            assert (x[:mark] == 0x5A5A5A5A).all() and (x[mark + n:] == 0x5A5A5A5A).all(), cu
+        assert (ws[need.value:] == 0x5A).all(), cu
+        got = accepted[mark:mark + n_seq].tolist()
+        assert all(0 <= x <= n_draft for x in got), cu
+        if cu == [0, 2, 5, 6]:
+            assert (tokens[mark:mark + n_draft + n_seq].tolist(), got) == _declared(s)
