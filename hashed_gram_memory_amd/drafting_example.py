@@ -130,12 +130,16 @@ class Drafting:
 
 
 def prompts_in(layer: Layer, prompts: list[torch.Tensor]):
-    """Prompts into the cache in one call, but for the last token of each: (that token, the three before it)."""
+    """Prompts into the cache in one call, but for the last token of each: (that token, the three before it).  Refused where
+    the pool or a table does not hold them all; the requests' lengths are then as they were."""
     new = [p.numel() - 1 for p in prompts]
     q, k, v = (torch.cat(x) for x in zip(*(layer.project(p[None]) for p in prompts)))
     keep = torch.cat([torch.arange(p.numel(), device="cuda") < p.numel() - 1 for p in prompts])
     counts = torch.tensor(new, dtype=torch.int32, device="cuda")
     positions, cu_q, kv_len = layer.pool.place(counts, sum(new))
+    short = (kv_len != counts).nonzero()[:, 0].tolist()
+    if short:  # without its prompt a request would go on from its last token alone
+        raise RuntimeError(f"no room for the prompts of the requests {short}: more pages or a wider table are needed")
     if sum(new):
         layer.attend(q[keep], k[keep], v[keep], positions, cu_q, kv_len, max(new))
     layer.pool.lengths.copy_(kv_len)
