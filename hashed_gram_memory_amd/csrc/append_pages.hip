@@ -546,7 +546,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void a
     }
 }
 
-// One token a request: a wave takes RPW (head, side) pairs of it.
+// One token a request, its first (others are past max_q_len): a wave takes RPW (head, side) pairs of it.
 template <class T, int D, class C>
 __global__ __launch_bounds__(256) void append_token_kernel(const AppendPagesArgs A, uint32_t steps) {
     constexpr int LPH = D / 16;
@@ -556,7 +556,7 @@ __global__ __launch_bounds__(256) void append_token_kernel(const AppendPagesArgs
     const uint32_t item = blockIdx.x * 4u + wave, b = item / steps;
     if (b >= A.n_seq) return;
     const Fresh req = fresh_of(A, b);
-    if (req.q_len != 1u || req.kv_len == 0) return;
+    if (req.q_len == 0u || req.first < 0) return;
     const uint32_t tok = req.q0, heads = A.cache.n_kv_heads, shift = A.cache.page_shift;
     const uint32_t pair = (item - b * steps) * RPW + lane / LPH;
     const bool live = pair < 2u * heads;
@@ -571,7 +571,7 @@ __global__ __launch_bounds__(256) void append_token_kernel(const AppendPagesArgs
         raw[0] = *reinterpret_cast<const u32x4v*>(src + bl.b0 * 8u);
         raw[1] = *reinterpret_cast<const u32x4v*>(src + bl.b1 * 8u);
     }
-    const uint32_t key = static_cast<uint32_t>(req.kv_len - 1), place = key & ((1u << shift) - 1u);
+    const uint32_t key = static_cast<uint32_t>(req.first), place = key & ((1u << shift) - 1u);
     const int64_t page = A.table[b * A.table_stride + (key >> shift)];
     if (page < 0 || page >= A.cache.n_pages) return;
     float* const scale = (side ? A.cache.v_scale : A.cache.k_scale) + page * heads + head;

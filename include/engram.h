@@ -555,8 +555,8 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  * Rows of a page before a request's first new token count as held, those after
  * its last do not and are left as they are: a request whose tokens were
  * refused appends over them.  A token before the request's first key, and one
- * on a page number outside the pool, is left out; those past max_q_len (0: not
- * known) of a request may be.  kv_len is bounded by table_width *
+ * on a page number outside the pool, is left out; those past the first max_q_len
+ * (0: not known) of a request may be.  kv_len is bounded by table_width *
  * page_size, by 2^31 - 4096 and by 0.  A page is written for one request:
  * two requests of a call must not append to the same page.
  *
