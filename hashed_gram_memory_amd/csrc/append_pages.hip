@@ -56,6 +56,7 @@ struct CodeE4m3 {
         const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * by, x[1] * by, 0, false);
         return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * by, x[3] * by, lo, true));
     }
+    static __device__ __forceinline__ uint32_t again(const float* x, float ratio) { return four(x, ratio); }
     static __device__ __forceinline__ void values(uint32_t w, float* x) {
         const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
         const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
@@ -68,6 +69,13 @@ struct CodeE4m3 {
 struct CodeI8 {
     // |x| <= largest = (127 / 64) * 2^6
     static constexpr uint32_t kMantissa = 0x7E0000u, kExponent = 6u;
+    // Codes held, times a ratio of -1 to 1; -128, which no append writes, is -127 where the sign changes.
+    static __device__ __forceinline__ uint32_t again(const float* x, float ratio) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = ratio < 0.0f ? fmaxf(x[i], -127.0f) : x[i];
+        return four(y, ratio);
+    }
     static __device__ __forceinline__ uint32_t four(const float* x, float by) {
         // 1.5 * 2^23 leaves the whole number nearest to the product (ties to even) in the low bits: one rounding, as the
         // product is inside of the fused step
@@ -99,10 +107,11 @@ struct Scale {
 };
 __device__ __forceinline__ Scale grown(float need, float old, bool held) {
     Scale s;
+    const bool more = held && need > fabsf(old);  // (a scale from elsewhere may be negative, and stays so)
     // a NaN on either side stays
-    s.now = held ? (need > old || need != need ? need : old) : need;
+    s.now = more || !held || need != need ? need : old;
     s.by = s.now == 0.0f ? 0.0f : 1.0f / s.now;
-    s.ratio = held && s.now > old ? old * s.by : 1.0f;
+    s.ratio = more ? old * s.by : 1.0f;
     return s;
 }
 
@@ -119,7 +128,7 @@ __device__ __forceinline__ u32x4v again(u32x4v w, float ratio) {
     for (int i = 0; i < 4; ++i) {
         float x[4];
         C::values(w[i], x);
-        w[i] = C::four(x, ratio);
+        w[i] = C::again(x, ratio);
     }
     return w;
 }

@@ -546,12 +546,14 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  * rows x (fp32, M = 448 for e4m3, 127 for int8):
  *     need  = the least power of two (2^-126 at least) with max|x| <= need * M,
  *             0 for a page of zeros, NaN where an x is infinite or NaN
- *     scale = need where the first new row is the page's first, else the
- *             larger of need and the scale held; a NaN stays
+ *     scale = need where the first new row is the page's first, else need where
+ *             that is above the magnitude of the scale held, else that scale; a
+ *             NaN stays
  *     codes = x / scale, rounded to nearest, ties to even; where the scale grew,
  *             codes of the rows held before are multiplied by old / new and
  *             rounded again (codes under a scale that is 0 or NaN: unspecified
- *             but for zeros under 0)
+ *             but for zeros under 0); int8 codes of -128 count as -127 where a
+ *             negative scale gives way
  * Rows of a page before a request's first new token count as held, those after
  * its last do not and are left as they are: a request whose tokens were
  * refused appends over them.  A token before the request's first key, and one
