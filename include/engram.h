@@ -552,8 +552,10 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  *     codes = x / scale, rounded to nearest, ties to even; where the scale grew,
  *             codes of the rows held before are multiplied by old / new and
  *             rounded again (codes under a scale that is 0 or NaN: unspecified
- *             but for zeros under 0); int8 codes of -128 count as -127 where a
- *             negative scale gives way
+ *             but for zeros under 0).  Under a scale from elsewhere that is no
+ *             power of two x is multiplied by 1 / scale, rounded to fp32, so that
+ *             next to a border it may have the neighbouring code; int8 codes of
+ *             -128 count as -127 where a negative scale gives way.
  * Rows of a page before a request's first new token count as held, those after
  * its last do not and are left as they are: a request whose tokens were
  * refused appends over them.  A token before the request's first key, and one
