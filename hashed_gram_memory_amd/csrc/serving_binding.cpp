@@ -541,28 +541,22 @@ PyObject* page_tables(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
         d.n_tok = a.number(7);
         if (d.n_tok < 0) refuse("n_tok is negative");
         const bool size_only = a.truth(9);
-        at::Tensor slots, positions, cu_q, kv_len, n_short;
-        static int64_t nothing[2];  // stands for outputs that are not there yet, where only their sizes are looked at
-        if (size_only) {
-            d.slots = nothing;
-            d.positions = d.cu_q = d.kv_len = d.n_short = reinterpret_cast<int32_t*>(nothing);
-        } else {
-            Parts parts(a.device, Parts::room(8 * d.n_tok) + Parts::room(4 * d.n_tok) + Parts::room(4 * d.n_seq + 4) +
-                                      Parts::room(4 * d.n_seq) + 16);
-            slots = parts.part(at::kLong, d.n_tok);
-            positions = parts.part(at::kInt, d.n_tok);
-            cu_q = parts.part(at::kInt, d.n_seq + 1);
-            kv_len = parts.part(at::kInt, d.n_seq);
-            n_short = parts.part(at::kInt, 1);
-            d.slots = static_cast<int64_t*>(slots.data_ptr());
-            d.positions = static_cast<int32_t*>(positions.data_ptr());
-            d.cu_q = static_cast<int32_t*>(cu_q.data_ptr());
-            d.kv_len = static_cast<int32_t*>(kv_len.data_ptr());
-            d.n_short = static_cast<int32_t*>(n_short.data_ptr());
-        }
+        static int64_t nothing[2];  // stands for outputs that are not there yet: sizes are looked at before any is allocated
+        d.slots = nothing;
+        d.positions = d.cu_q = d.kv_len = d.n_short = reinterpret_cast<int32_t*>(nothing);
         size_t need = 0;
-        check(engram_page_tables_workspace(&d, &need), "engram_page_tables_workspace");
+        check(engram_page_tables_workspace(&d, &need), size_only ? "engram_page_tables_workspace" : "engram_page_tables");
         if (size_only) return PyLong_FromSize_t(need);
+        Parts parts(a.device, Parts::room(8 * d.n_tok) + Parts::room(4 * d.n_tok) + Parts::room(4 * d.n_seq + 4) +
+                                  Parts::room(4 * d.n_seq) + 16);
+        const at::Tensor slots = parts.part(at::kLong, d.n_tok), positions = parts.part(at::kInt, d.n_tok);
+        const at::Tensor cu_q = parts.part(at::kInt, d.n_seq + 1), kv_len = parts.part(at::kInt, d.n_seq);
+        const at::Tensor n_short = parts.part(at::kInt, 1);
+        d.slots = static_cast<int64_t*>(slots.data_ptr());
+        d.positions = static_cast<int32_t*>(positions.data_ptr());
+        d.cu_q = static_cast<int32_t*>(cu_q.data_ptr());
+        d.kv_len = static_cast<int32_t*>(kv_len.data_ptr());
+        d.n_short = static_cast<int32_t*>(n_short.data_ptr());
         const Workspace ws = workspace_of(a, 8, need);
         launch(a, "engram_page_tables", [&](void* stream) { return engram_page_tables(&d, ws.p, ws.bytes, stream); });
         return pack({slots, positions, cu_q, kv_len, n_short});
