@@ -44,8 +44,9 @@
 //
 // What it measured, for 2,048 tokens at the end of 32,768 keys, 32 heads over 8
 // of head_dim 128, bf16: 1,314 us with two buffers, staged through registers,
-// and no turns; 1,050 to 1,100 us as it stands, 1.01 PFLOP/s at the most, where
-// a product of 8192^3 reached 1.25 to 1.37 on the same card.  A turn's products
+// and no turns; 1,000 to 1,050 us as it stands, 1.06 PFLOP/s at the most, where
+// a product of 8192^3 reached 1.25 to 1.37 on the same card (with the places of
+// keys in 64 bits, 16 compares of a turn, 1,034 to 1,083).  A turn's products
 // take 1,900 cycles of a wave for 1,190 that they take alone: LDS answers
 // products and the other half's softmax issues between them.  Of the time,
 // about a sixth is the card's power: zeros for q, K and V run that much faster.
@@ -56,12 +57,12 @@
 // 2.1e-4 in fp16).  Twice the digits, as in paged_rows.hip, are half as many
 // products again, and here the products are what is waited for: with them the
 // chunk took 1,450 us for 1,097, the batch of 24 requests 72.0 for 62.7, the
-// chunk of head_dim 64 893 for 699.  Codes of bf16 queries do not need them: a
-// code is exact in fp16, and so P is, V's scales being powers of two near each
-// other (Near), an fp16 of 11 bits for bf16's 8; the output of the int8 chunk is
-// then off by what its own rounding does, 1.7e-3 of it for 2.2e-3.  The scales
-// are looked at before the first tile (1 to 2 us of a short call); the loop takes
-// the same instructions.
+// chunk of head_dim 64 893 for 699.  Pages of codes do not need them for bf16
+// queries: a code is exact in fp16, and where V's scales are powers of two near
+// each other (Near), P is an fp16 of 11 bits for bf16's 8.  The output of the int8
+// chunk is then off by what its own rounding does, 1.7e-3 for 2.2e-3.  The scales
+// are looked at before the first tile (0.3 us of a short call); the loop takes the
+// same instructions.
 //
 // What a row does not see: scores of hidden keys become -inf before the
 // maximum, and their p is 0.  A key that no row sees (past the end, before the
@@ -166,6 +167,20 @@ __device__ __forceinline__ uint32_t near_of(float scale) {
 __device__ __forceinline__ uint32_t near_both(uint32_t a, uint32_t b) {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2t, a), __builtin_bit_cast(u16x2t, b)));
 }
+// Of a wave's lanes, exchanged without LDS.
+__device__ __forceinline__ uint32_t near_wave(uint32_t x) {
+    const auto dpp = [&](auto control) {
+        x = near_both(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), decltype(control)::value, 0xF, 0xF, true)));
+    };
+    dpp(std::integral_constant<int, 0xB1>());  // the neighbour, the pair beside it, and rows of 8 and of 16 mirrored
+    dpp(std::integral_constant<int, 0x4E>());
+    dpp(std::integral_constant<int, 0x141>());
+    dpp(std::integral_constant<int, 0x140>());
+    const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = near_both(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return near_both(static_cast<uint32_t>(b[0]), static_cast<uint32_t>(b[1]));
+}
 __device__ __forceinline__ Near near_scales(uint32_t x, uint32_t keys) {
     const int32_t top = static_cast<int32_t>(x & 0xFFFFu), low = 256 - static_cast<int32_t>(x >> 16);
     const int32_t most = min(kNear, kNear + 17 - (32 - __builtin_clz(max(keys, 2u) - 1u)));
@@ -178,7 +193,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
     constexpr bool kE4m3 = kHeld != kHalves;        // codes, of either kind
     constexpr bool kPages = kHeld == kE4m3Pages || kHeld == kI8Pages;  // one scale for a page and head
     // A page's scale goes into its numbers as they are widened where bf16's range holds them: by way of the softmax, a chunk of
-    // 2,048 tokens over 32,768 keys took 1,375 us for 1,190 with e4m3 and 1,425 for 1,199 with int8.
+    // 2,048 tokens over 32,768 keys took 1,375 us with e4m3 where this took 1,190, and 1,425 for 1,199 with int8 (now 1,150 to
+    // 1,160 and 1,177 to 1,192).
     constexpr bool kFold = kPages && std::is_same_v<T, Bf16>;
     constexpr bool kScales = kE4m3 && !kFold;       // scales by way of LDS to the scores and weights
     constexpr uint32_t kRows = kWaves * 32u, kThreads = kWaves * 64u;
@@ -631,8 +647,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(D =
                 if (!none) spread = near_both(spread, near_of(A.cache.v_scale[static_cast<int64_t>(p) * heads + h]));
         }
         if constexpr (kFold) {
-#pragma unroll
-            for (int k = 1; k < 64; k <<= 1) spread = near_both(spread, static_cast<uint32_t>(__shfl_xor(static_cast<int>(spread), k)));
+            spread = near_wave(spread);
             if (lane == 0) sm_spread[wave] = spread;
         }
         all_there = !__syncthreads_or(bad);
