@@ -564,6 +564,12 @@ int engram_kv_append(const engram_append_desc* desc, void* stream);
  * page_size, by 2^31 - 4096 and by 0.  A page is written for one request:
  * two requests of a call must not append to the same page.
  *
+ * A token that is taken back, as a refused draft is, leaves its mark on its
+ * page: the scale that it raised stays, for the rows held, which were rounded
+ * again under it, and for those that follow; an infinity or NaN in it leaves the
+ * page's scale, and so all rows of that page and head, NaN.  Both end when the
+ * page's first row is written anew.
+ *
  * n_tok == 0 is a no-op.  Errors: EINVAL, ERANGE (n_tok / page_size + 2 n_seq
  * pages times n_kv_heads / 2, or n_seq * n_kv_heads of single tokens, may be
  * refused above 2^23: split the batch), EUNSUPPORTED (a type
