@@ -36,6 +36,8 @@
 //     128 and 256) the maximum is found first, and they are read and turned
 //     again.  (Pages of 64 read twice took 58 us; eight steps held by one wave as
 //     they were read took all registers, 86.)
+//     Four waves on a SIMD leave 128 registers: int8 takes 126, e4m3 spills 4 (12
+//     bytes of scratch a lane).
 //   * Single tokens: a wave takes as many (head, side) pairs of a token as it
 //     holds rows.
 #include <algorithm>

@@ -22,7 +22,7 @@ struct AttentionArgs {
     CacheView cache;
     // Parts of divided rows, not yet divided by their sums: sums of values, and (reference r, sum of weights) in
     // units of 2^(x - r).  paged_tile.hip: [n_split][n_tok][n_q_heads][dim or 2]; paged_rows.hip: [n_work][2]
-    // [min(max_rows, 16)][dim or 2], and what there is to join.
+    // [min(max_rows, of_tile)][dim or 2], and what there is to join.
     float* part_o;
     float* part_ml;
     int4* part_job;          // [n_work]
@@ -38,7 +38,7 @@ struct AttentionArgs {
     uint32_t n_split;        // splits of a tile at most
     uint32_t n_work;         // paged_rows.hip: workgroups that share the keys evenly; 0: a workgroup takes a tile
     uint32_t min_rows, max_rows;  // requests of this launch: min_rows <= rows <= max_rows
-    uint32_t of_tile;        // paged_tile.hip: rows of a tile, kFullTile or kHalfTile
+    uint32_t of_tile;        // rows of a tile; paged_tile.hip: kFullTile or kHalfTile, paged_rows.hip: kRowsTile or twice that
     uint32_t tiles_per;      // tiles set aside for each request; 0: as the lengths need (find_tile)
     float scale_log2;        // scale * log2(e)
 };

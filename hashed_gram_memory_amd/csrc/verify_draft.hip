@@ -12,9 +12,9 @@
 //
 // The work is the reading of one row of p, and of q where a draft was refused:
 // HBM-bound for a batch, latency for one request.  64 requests of 5 drafts over
-// 129,280 words in fp32, 9 of 10 with a refused draft, take 19.2 us: 12 us of
-// sums (62 MB, 5.2 TB/s) and 7 to choose the word; one request takes 10.1 us,
-// over 4,096 words 6.4.
+// 129,280 words in fp32, 9 of 10 with a refused draft, take 19 to 20 us: 12 us of
+// sums (62 MB, 5.3 TB/s) and 7.6 to choose the word; one request over 32,768
+// words takes 9.5 to 10 us, over 4,096 words 6.4.
 //
 // Mapping: a row is taken in blocks of 4,096 words, 16 neighbours to each of
 // 256 threads.  One launch sums the blocks, a second finds the block in which
