@@ -115,3 +115,29 @@ def test_far_scales_beside_near_ones():
     assert torch.equal(got[0][100:200], want[0][100:200])
     for b in (0, 2):
         _compare(_one(s, b), (got[0][100 * b:100 * b + 100], got[1][100 * b:100 * b + 100]), 0, 400)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_small_weights_of_many_keys(kind, dim):
+    """A key whose value is 0 outweighs all others by 2^20 to 2^34, which the output is made of: powers of two, which fp16
+    holds down to 2^-24 of weights that are 2^10 at their row's largest, so that nothing but the output is rounded."""
+    page, new, length = 16, 60, 3000
+    s = _coded(7, kind, BF16, dim, 1, 1, page, [new], [length])
+    one = 64 if kind == "int8" else 0x78  # 64 * 2^-6, 256 * 2^-8: 1
+    unit = 2.0 ** -6 if kind == "int8" else 2.0 ** -8
+    s["q"].zero_()
+    far = torch.arange(new) % 15 + 20  # powers of two below the first key
+    s["q"][:, 0, 0] = far.to(BF16)
+    for x in "kv":
+        s[x].zero_()
+        s[x + "_scale"][:] = unit
+    s["k"][..., 0] = -64 if kind == "int8" else one | 0x80  # -1: a score of -far
+    s["v"][:] = one
+    p = int(s["table"][0, 0])
+    s["k"][p, 0, 0], s["v"][p, 0, 0] = 0, 0
+    got = _attend(s, scale=math.log(2.0), max_q_len=new)[0].double().cpu()[:, 0]
+    others = (torch.arange(length - new, length)).double() * torch.exp2(-far.double())
+    want = (others / (1 + others))[:, None]
+    # scores of up to 34 are off by a few fp32 steps each, and so weights by 34 times as much of themselves
+    assert ((got - want).abs() <= want * (so.half_step(BF16) + 64 * 34 * so.U32)).all(), (got[:, 0] / want[:, 0] - 1).abs().max()
